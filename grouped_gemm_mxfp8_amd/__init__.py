@@ -9,6 +9,7 @@ functions raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -45,6 +46,8 @@ _SIGS = {
     "mx_validate_offsets": (_I32, [_P, _I32, _I64]),
     "mxfp8_quantize": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _P, _I64, _P, _P]),
     "grouped_linear_fwd": (_I32, [_I32, _P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
+    "mxfp4_quantize": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
+    "mxfp4_dequantize": (_I32, [_P, _P, _I64, _I64, _P, _P]),
     "fp8_tensor_quantize": (_I32, [_P, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _P]),
     "grouped_linear_fwd_fp8": (_I32, [_P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
     "grouped_mlp_fwd": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P,
@@ -180,6 +183,84 @@ def mxfp8_quantize(x: torch.Tensor, rowwise: bool = True, colwise: bool = False,
                               _ptr(cc), _ptr(cs), ld, _ptr(poff), _stream(dev))
     _check("mxfp8_quantize", st)
     return out
+
+
+@dataclasses.dataclass
+class Mx4Tensor:
+    """MXFP4 operand [..., C]: E2M1 codes, two a byte (uint8 [..., C/2]), and
+    E8M0 scales (uint8 [..., C/32])."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def _on(dev):
+    """Makes ``dev`` the current device for a library call (a no-op where it is)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else \
+        torch.cuda.device(dev)
+
+
+def mxfp4_quantize(x: torch.Tensor, rowwise: bool = True, colwise: bool = False):
+    """Block-quantize bf16 ``x`` ([R, C] or [batch, R, C]) to MXFP4.
+
+    Returns a dict with ``row`` (Mx4Tensor [.., R, C/2] / [.., R, C/32]) and/or
+    ``col`` (the transposed copy, blocks along R: Mx4Tensor [.., C, R/2] /
+    [.., C, R/32], R a multiple of 32).  C is a multiple of 32."""
+    _need(x, torch.bfloat16, "x")
+    dev = x.device
+    if x.dim() == 2:
+        (R, C), lead, batch = x.shape, (), 1
+    elif x.dim() == 3:
+        batch, R, C = x.shape
+        lead = (batch,)
+    else:
+        raise ValueError("x must be 2-D or 3-D")
+    if batch == 0:
+        raise ValueError("x has no matrices")
+    out = {}
+    rc = rs = cc = cs = None
+    if rowwise:
+        rc = torch.empty((*lead, R, C // 2), dtype=torch.uint8, device=dev)
+        rs = torch.empty((*lead, R, C // BLOCK), dtype=torch.uint8, device=dev)
+        out["row"] = Mx4Tensor(rc, rs)
+    if colwise:
+        cc = torch.empty((*lead, C, R // 2), dtype=torch.uint8, device=dev)
+        cs = torch.empty((*lead, C, R // BLOCK), dtype=torch.uint8, device=dev)
+        out["col"] = Mx4Tensor(cc, cs)
+    if x.numel() == 0:           # nothing to launch (empty tensors have no address)
+        if not out:
+            raise ValueError("rowwise or colwise must be requested")
+        if C % BLOCK or (colwise and R % BLOCK):
+            raise ValueError(f"C (and R of a columnwise copy) must be multiples of {BLOCK}")
+        return out
+    with _on(dev):
+        st = lib().mxfp4_quantize(_ptr(x), batch, R, C, _ptr(rc), _ptr(rs), _ptr(cc), _ptr(cs),
+                                  _stream(dev))
+    _check("mxfp4_quantize", st)
+    return out
+
+
+def _need_mx4(q, name, dev=None):
+    """Checks an MXFP4 operand; returns the number of values in a row."""
+    _need(q.codes, torch.uint8, name + ".codes", dev)
+    _need(q.scales, torch.uint8, name + ".scales", q.codes.device)
+    C = 2 * q.codes.shape[-1]
+    if C % BLOCK or tuple(q.scales.shape) != (*q.codes.shape[:-1], C // BLOCK):
+        raise ValueError(f"{name}: scales {tuple(q.scales.shape)} do not fit codes "
+                         f"{tuple(q.codes.shape)} (one scale per {BLOCK} values)")
+    return C
+
+
+def mxfp4_dequantize(q: Mx4Tensor) -> torch.Tensor:
+    """The values that MXFP4 codes and scales stand for, bf16 (exact)."""
+    C = _need_mx4(q, "q")
+    dev = q.codes.device
+    y = torch.empty((*q.codes.shape[:-1], C), dtype=torch.bfloat16, device=dev)
+    if y.numel():
+        with _on(dev):
+            st = lib().mxfp4_dequantize(_ptr(q.codes), _ptr(q.scales), y.numel() // C, C, _ptr(y),
+                                        _stream(dev))
+        _check("mxfp4_dequantize", st)
+    return y
 
 
 def grouped_linear_fwd(x, offsets: torch.Tensor, w, row_scale: Optional[torch.Tensor] = None):
@@ -616,6 +697,7 @@ def combine_bwd(dout: torch.Tensor, row_of: torch.Tensor, M: int,
 
 
 __all__ = ["lib", "last_error", "MxError", "MxTensor", "MlpCtx", "mxfp8_quantize",
+           "Mx4Tensor", "mxfp4_quantize", "mxfp4_dequantize",
            "grouped_linear_fwd", "fp8_tensor_quantize", "grouped_linear_fwd_fp8", "Fp8Tensor",
            "grouped_mlp_fwd", "grouped_mlp_bwd", "padded_rows_bound",
            "ws_mx_view", "ctx_bytes", "fwd_ws_bytes", "bwd_ws_bytes", "router", "route_plan",

@@ -624,6 +624,80 @@ mx_status grouped_linear_fwd_fp8(const uint8_t* x, const float* d_x_scale_inv,
 
 constexpr uint32_t kFwdFlags = MX_FWD_REUSE_WEIGHTS | MX_MLP_SAVE_H;
 
+// ---- MXFP4 ---------------------------------------------------------------------
+namespace {
+constexpr int64_t kMx4MaxValues = (int64_t)1 << 44;   // flat launches of 8192 values a workgroup
+
+// a * b <= limit for non-negative a, b, without overflow
+bool product_within(int64_t a, int64_t b, int64_t limit) { return a == 0 || b <= limit / a; }
+}  // namespace
+
+mx_status mxfp4_quantize(const void* x, int64_t batch, int64_t R, int64_t C, uint8_t* row_codes,
+                         uint8_t* row_scales, uint8_t* col_codes, uint8_t* col_scales,
+                         mx_stream_t stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (batch < 1 || R < 0 || C < 0)
+        return fail(MX_ERR_INVALID_ARG, "mxfp4_quantize: bad sizes batch=%lld R=%lld C=%lld",
+                    (long long)batch, (long long)R, (long long)C);
+    const bool want_row = row_codes || row_scales, want_col = col_codes || col_scales;
+    if (want_row && !(row_codes && row_scales))
+        return fail(MX_ERR_INVALID_ARG, "mxfp4_quantize: row_codes and row_scales go together");
+    if (want_col && !(col_codes && col_scales))
+        return fail(MX_ERR_INVALID_ARG, "mxfp4_quantize: col_codes and col_scales go together");
+    if (!want_row && !want_col)
+        return fail(MX_ERR_INVALID_ARG, "mxfp4_quantize: no output requested");
+    if (!x) return fail(MX_ERR_INVALID_ARG, "mxfp4_quantize: x is NULL");
+    if (C % 32)
+        return fail(MX_ERR_UNSUPPORTED, "mxfp4_quantize: C=%lld is not a multiple of 32", (long long)C);
+    if (want_col && R % 32)
+        return fail(MX_ERR_UNSUPPORTED, "mxfp4_quantize: the columnwise copy needs R %% 32 == 0, got %lld",
+                    (long long)R);
+    if (!aligned(x, 16) || !aligned(row_codes, 16) || !aligned(col_codes, 16))
+        return fail(MX_ERR_INVALID_ARG, "mxfp4_quantize: x and codes must be 16-byte aligned");
+    if (!product_within(batch, R, kMx4MaxValues) || !product_within(batch * R, C, kMx4MaxValues))
+        return fail(MX_ERR_UNSUPPORTED, "mxfp4_quantize: tensor too large");
+    if (want_col && (batch > 65535 || C > (int64_t)64 * 65535))
+        return fail(MX_ERR_UNSUPPORTED, "mxfp4_quantize: batch or C too large for the columnwise copy");
+    const int64_t n = batch * R * C;
+    if (n == 0) return ok();
+    const uint16_t* xs = static_cast<const uint16_t*>(x);
+    const double bytes = (2.0 + 17.0 / 32) * (double)n;
+    if (want_row) {
+        const mx_status st = launched(
+            timed("quant4_rows", bytes, MX_WORK_BYTES, s,
+                  [&] { return mx::launch_quant4_rows(xs, n, row_codes, row_scales, s); }),
+            "quant4_rows");
+        if (st != MX_OK || !want_col) return st;
+    }
+    return launched(timed("quant4_cols", bytes, MX_WORK_BYTES, s,
+                          [&] {
+                              return mx::launch_quant4_cols(xs, batch, R, C, col_codes, col_scales, s);
+                          }),
+                    "quant4_cols");
+}
+
+mx_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t C,
+                           void* y, mx_stream_t stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (rows < 0 || C < 0)
+        return fail(MX_ERR_INVALID_ARG, "mxfp4_dequantize: bad sizes rows=%lld C=%lld", (long long)rows,
+                    (long long)C);
+    if (C % 32)
+        return fail(MX_ERR_UNSUPPORTED, "mxfp4_dequantize: C=%lld is not a multiple of 32", (long long)C);
+    if (!product_within(rows, C, kMx4MaxValues))
+        return fail(MX_ERR_UNSUPPORTED, "mxfp4_dequantize: tensor too large");
+    if (rows * C == 0) return ok();
+    if (!codes || !scales || !y) return fail(MX_ERR_INVALID_ARG, "mxfp4_dequantize: NULL argument");
+    if (!aligned(codes, 16) || !aligned(y, 16))
+        return fail(MX_ERR_INVALID_ARG, "mxfp4_dequantize: codes and y must be 16-byte aligned");
+    return launched(timed("dequant4", (2.0 + 17.0 / 32) * (double)(rows * C), MX_WORK_BYTES, s,
+                          [&] {
+                              return mx::launch_dequant4(codes, scales, rows * C,
+                                                         static_cast<uint16_t*>(y), s);
+                          }),
+                    "dequant4");
+}
+
 size_t grouped_mlp_ctx_bytes(int64_t M, int64_t H, int64_t F, int32_t E, uint32_t flags) {
     MlpDims d;
     if ((flags & ~(uint32_t)MX_MLP_SAVE_H) || check_mlp_dims(M, H, F, E, &d) != MX_OK) return 0;

@@ -167,6 +167,20 @@ hipError_t launch_fp8_tensor_quant(const uint16_t* x, int64_t rows, int64_t C,
                                    const int64_t* offs, int G, int64_t R, uint32_t* amax,
                                    uint8_t* codes, float* scale_inv, hipStream_t s);
 
+// ---- MXFP4 -------------------------------------------------------------------
+// Blocks of 32 E2M1 codes (two a byte, the even element low) with one E8M0
+// scale.  n values of whole blocks, flat; x and y 16-byte, codes 4-byte
+// aligned; n / 8192 < 2^31.
+hipError_t launch_quant4_rows(const uint16_t* x, int64_t n, uint8_t* codes, uint8_t* scales,
+                              hipStream_t s);
+hipError_t launch_dequant4(const uint8_t* codes, const uint8_t* scales, int64_t n, uint16_t* y,
+                           hipStream_t s);
+// Columnwise copy of x [batch][R][C]: codes [batch][C][R/2], scales
+// [batch][C][R/32]; R % 32 == 0, C % 32 == 0, 16-byte aligned codes,
+// batch <= 65535, C <= 64 * 65535.
+hipError_t launch_quant4_cols(const uint16_t* x, int64_t batch, int64_t R, int64_t C, uint8_t* codes,
+                              uint8_t* scales, hipStream_t s);
+
 int device_cu_count();
 
 }  // namespace mx

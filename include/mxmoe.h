@@ -187,6 +187,35 @@ mx_status grouped_linear_fwd_fp8(const uint8_t* x, const float* d_x_scale_inv,
                                  mx_stream_t stream);
 
 /*
+ * MXFP4, the 4-bit format of the microscaling family that MXFP8 belongs to
+ * (OCP Microscaling formats, version 1.0): two E2M1 codes a byte (the even
+ * element in the low half; values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives) and one E8M0 scale per 32 values along the last axis.  The scale
+ * of a block is 2^max(floor(log2(amax)) - 2, -127); elements are rounded to
+ * nearest even and saturate at +-6, the sign kept for values that round to
+ * zero.  A block with an infinity or a NaN gets scale 255 (NaN) and codes 0.
+ *
+ * mxfp4_quantize -- bf16 x [batch][R][C], C % 32 == 0:
+ *   row_codes   uint8 [batch][R][C/2] and row_scales [batch][R][C/32]: blocks
+ *               along C.  Both NULL to skip.
+ *   col_codes   uint8 [batch][C][R/2] and col_scales [batch][C][R/32]: the
+ *               transposed copy, blocks along R, R % 32 == 0 (for weights
+ *               [E][N][K]: the operand of the data gradient, see
+ *               grouped_linear_fwd).  Both NULL to skip.  batch <= 65535.
+ *   At least one copy.  x and codes 16-byte aligned.  x must not overlap an
+ *   output.
+ * mxfp4_dequantize -- bf16 y [rows][C] of codes [rows][C/2] and scales
+ *   [rows][C/32], C % 32 == 0; every value is exact, a block with scale 255
+ *   gives NaN.  codes and y 16-byte aligned.
+ * rows * C below 2^44 in both.
+ */
+mx_status mxfp4_quantize(const void* x, int64_t batch, int64_t R, int64_t C, uint8_t* row_codes,
+                         uint8_t* row_scales, uint8_t* col_codes, uint8_t* col_scales,
+                         mx_stream_t stream);
+mx_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t C,
+                           void* y, mx_stream_t stream);
+
+/*
  * grouped_mlp_fwd -- fused GroupedMLP forward (German page, the paragraph on
  * the GroupedMLP fusion kernel; Portuguese page, third paragraph; French page,
  * third improvement), in the order gate-up projection -> SwiGLU -> routing
