@@ -24,6 +24,9 @@ LIB_PATH = os.environ.get("MXMOE_LIB") or os.path.join(HERE, "libmxmoe.so")
 
 MX_DTYPE_BF16 = 0
 MX_DTYPE_MXFP8 = 1
+MX_DTYPE_MXFP4 = 2
+MX_DTYPE_MXFP8_MXFP4 = 3
+MX_LAYER_MAX_TOKENS = 128
 TOKEN_ALIGN = 128
 BLOCK = 32
 MX_CTX_H, MX_CTX_XCOL, MX_CTX_ZCOL, MX_CTX_POFF, MX_CTX_W1COL, MX_CTX_W2COL = 0, 1, 2, 3, 4, 5
@@ -48,6 +51,9 @@ _SIGS = {
     "grouped_linear_fwd": (_I32, [_I32, _P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
     "mxfp4_quantize": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
     "mxfp4_dequantize": (_I32, [_P, _P, _I64, _I64, _P, _P]),
+    "moe_layer_ws_bytes": (_SZ, [_I32, _I64, _I32, _I32, _I64, _I64]),
+    "moe_layer_fwd": (_I32, [_I32, _P, _P, _I64, _I32, _I32, _I64, _I64, _P, _P, _P, _P, _P, _P,
+                             _SZ, _P]),
     "fp8_tensor_quantize": (_I32, [_P, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _P]),
     "grouped_linear_fwd_fp8": (_I32, [_P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
     "grouped_mlp_fwd": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P,
@@ -250,6 +256,17 @@ def _need_mx4(q, name, dev=None):
     return C
 
 
+def _need_mx8(q, name, dev=None):
+    """Checks an MXFP8 operand; returns the number of values in a row."""
+    _need(q.codes, torch.uint8, name + ".codes", dev)
+    _need(q.scales, torch.uint8, name + ".scales", q.codes.device)
+    C = q.codes.shape[-1]
+    if C % BLOCK or tuple(q.scales.shape) != (*q.codes.shape[:-1], C // BLOCK):
+        raise ValueError(f"{name}: scales {tuple(q.scales.shape)} do not fit codes "
+                         f"{tuple(q.codes.shape)} (one scale per {BLOCK} values)")
+    return C
+
+
 def mxfp4_dequantize(q: Mx4Tensor) -> torch.Tensor:
     """The values that MXFP4 codes and scales stand for, bf16 (exact)."""
     C = _need_mx4(q, "q")
@@ -267,8 +284,13 @@ def grouped_linear_fwd(x, offsets: torch.Tensor, w, row_scale: Optional[torch.Te
     """GroupedLinear: y[rows of e] = x[rows of e] @ w[e].T for every expert.
 
     ``x`` bf16 [M, K] and ``w`` bf16 [E, N, K], or both MxTensor (rowwise
-    MXFP8 copies).  Returns bf16 [M, N].
+    MXFP8 copies), or ``w`` an Mx4Tensor and ``x`` an Mx4Tensor or MxTensor
+    (MXFP4 weights with MXFP4 or MXFP8 activations).  Returns bf16 [M, N].
     """
+    if isinstance(w, Mx4Tensor):
+        return _linear_mxfp4(x, offsets, w, row_scale)
+    if isinstance(x, Mx4Tensor):
+        raise TypeError("MXFP4 activations need MXFP4 weights")
     if isinstance(x, MxTensor):
         if not isinstance(w, MxTensor):
             raise TypeError("x and w must both be MXFP8 or both bf16")
@@ -299,6 +321,38 @@ def grouped_linear_fwd(x, offsets: torch.Tensor, w, row_scale: Optional[torch.Te
     y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     st = lib().grouped_linear_fwd(dtype, _ptr(xc), _ptr(xs), _ptr(offsets), E, M, _ptr(wc),
                                   _ptr(ws), N, K, _ptr(row_scale), _ptr(y), _stream(dev))
+    _check("grouped_linear_fwd", st)
+    return y
+
+
+def _linear_mxfp4(x, offsets, w: Mx4Tensor, row_scale):
+    if isinstance(x, Mx4Tensor):
+        dtype, K = MX_DTYPE_MXFP4, _need_mx4(x, "x")
+    elif isinstance(x, MxTensor):
+        dtype, K = MX_DTYPE_MXFP8_MXFP4, _need_mx8(x, "x")
+    else:
+        raise TypeError("MXFP4 weights take MXFP4 or MXFP8 activations")
+    dev = x.codes.device
+    K2 = _need_mx4(w, "w", dev)
+    if x.codes.dim() != 2 or w.codes.dim() != 3:
+        raise ValueError("x must be [M, K] and w [E, N, K]")
+    if K2 != K:
+        raise ValueError(f"K mismatch: x has {K}, w has {K2}")
+    M, (E, N) = x.codes.shape[0], w.codes.shape[:2]
+    _need(offsets, torch.int64, "offsets", dev)
+    if offsets.numel() != E + 1:
+        raise ValueError("offsets must have E+1 entries")
+    if row_scale is not None:
+        _need(row_scale, torch.float32, "row_scale", dev)
+        if tuple(row_scale.shape) != (M,):
+            raise ValueError("row_scale must be [M]")
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    if M == 0:
+        return y
+    with _on(dev):
+        st = lib().grouped_linear_fwd(dtype, _ptr(x.codes), _ptr(x.scales), _ptr(offsets), E, M,
+                                      _ptr(w.codes), _ptr(w.scales), N, K, _ptr(row_scale),
+                                      _ptr(y), _stream(dev))
     _check("grouped_linear_fwd", st)
     return y
 
@@ -696,8 +750,66 @@ def combine_bwd(dout: torch.Tensor, row_of: torch.Tensor, M: int,
     return dy, dw
 
 
+# ---- the whole layer for a few tokens ----------------------------------------
+
+def _layer_weight(w, name, dev):
+    """(dtype, codes or bf16 tensor, scales or None, [E, rows, values]) of a weight."""
+    if isinstance(w, Mx4Tensor):
+        C = _need_mx4(w, name, dev)
+        dtype, t, s = MX_DTYPE_MXFP4, w.codes, w.scales
+    elif isinstance(w, MxTensor):
+        C = _need_mx8(w, name, dev)
+        dtype, t, s = MX_DTYPE_MXFP8, w.codes, w.scales
+    else:
+        _need(w, torch.bfloat16, name, dev)
+        dtype, t, s, C = MX_DTYPE_BF16, w, None, w.shape[-1]
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D")
+    return dtype, t, s, (t.shape[0], t.shape[1], C)
+
+
+def moe_layer_fwd(x: torch.Tensor, logits: torch.Tensor, w1, w2, k: int,
+                  ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A whole MoE layer for up to ``MX_LAYER_MAX_TOKENS`` tokens (inference):
+    top-``k`` routing of ``logits`` (fp32 [T, E]), gate-up, SwiGLU scaled by the
+    routing weight, down projection and combine.  ``x`` bf16 [T, H]; ``w1``
+    [E, 2F, H] and ``w2`` [E, H, F] both bf16 tensors, MxTensor or Mx4Tensor
+    (rowwise copies).  Returns bf16 [T, H].  A logit of -inf masks an expert; a
+    token with every logit at -inf gets zeros.  ``ws``: optional caller-owned
+    uint8 scratch (allocated when missing or too small)."""
+    _need(x, torch.bfloat16, "x")
+    dev = x.device
+    _need(logits, torch.float32, "logits", dev)
+    d1, t1, s1, (E, F2, H1) = _layer_weight(w1, "w1", dev)
+    d2, t2, s2, (E2, H2, F) = _layer_weight(w2, "w2", dev)
+    if d1 != d2:
+        raise TypeError("w1 and w2 must be of one format")
+    if x.dim() != 2 or logits.dim() != 2:
+        raise ValueError("x must be [T, H] and logits [T, E]")
+    T, H = x.shape
+    if H1 != H or H2 != H or E2 != E or F2 != 2 * F or tuple(logits.shape) != (T, E):
+        raise ValueError("shape mismatch: x [T,H], logits [T,E], w1 [E,2F,H], w2 [E,H,F]")
+    L = lib()
+    nws = L.moe_layer_ws_bytes(d1, T, E, k, H, F)
+    if nws == 0:
+        raise MxError("moe_layer_fwd", 2, last_error())
+    out = torch.empty_like(x)
+    if T == 0:
+        return out
+    if ws is None or ws.numel() < nws:
+        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+    else:
+        _need(ws, torch.uint8, "ws", dev)
+    with _on(dev):
+        st = L.moe_layer_fwd(d1, _ptr(x), _ptr(logits), T, E, k, H, F, _ptr(t1), _ptr(s1),
+                             _ptr(t2), _ptr(s2), _ptr(out), _ptr(ws), nws, _stream(dev))
+    _check("moe_layer_fwd", st)
+    return out
+
+
 __all__ = ["lib", "last_error", "MxError", "MxTensor", "MlpCtx", "mxfp8_quantize",
            "Mx4Tensor", "mxfp4_quantize", "mxfp4_dequantize",
+           "moe_layer_fwd",
            "grouped_linear_fwd", "fp8_tensor_quantize", "grouped_linear_fwd_fp8", "Fp8Tensor",
            "grouped_mlp_fwd", "grouped_mlp_bwd", "padded_rows_bound",
            "ws_mx_view", "ctx_bytes", "fwd_ws_bytes", "bwd_ws_bytes", "router", "route_plan",

@@ -471,6 +471,30 @@ static mx_status pad_operands(const char* fn, const uint8_t* x, const uint8_t* x
     return MX_OK;
 }
 
+// grouped_linear_fwd on MXFP4 weights.
+static mx_status linear_mxfp4(bool x_fp4, const void* x, const uint8_t* x_scales, const int64_t* d_offsets,
+                              int32_t E, int64_t M, const void* w, const uint8_t* w_scales, int64_t N,
+                              int64_t K, const float* d_row_scale, void* y, hipStream_t s) {
+    if (!x_scales || !w_scales)
+        return fail(MX_ERR_INVALID_ARG, "grouped_linear_fwd: MXFP4 needs x_scales and w_scales");
+    if (K % 32 || N % 32)
+        return fail(MX_ERR_UNSUPPORTED, "grouped_linear_fwd: MXFP4 needs K %% 32 == 0 and N %% 32 == 0");
+    if (K > kI32Max || N > kI32Max)
+        return fail(MX_ERR_UNSUPPORTED, "grouped_linear_fwd: operand too large");
+    if (!aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(y, 16))
+        return fail(MX_ERR_INVALID_ARG,
+                    "grouped_linear_fwd: y must be 16-byte aligned and scales 4-byte aligned");
+    if (M == 0) return ok();
+    return launched(timed("linear4_few", 2.0 * M * N * K, MX_WORK_FLOP, s,
+                          [&] {
+                              return mx::launch_linear4_few(
+                                  x_fp4, static_cast<const uint8_t*>(x), x_scales, d_offsets, E, M,
+                                  static_cast<const uint8_t*>(w), w_scales, N, K, d_row_scale,
+                                  static_cast<uint16_t*>(y), s);
+                          }),
+                    "linear4_few");
+}
+
 mx_status grouped_linear_fwd(int32_t dtype, const void* x, const uint8_t* x_scales,
                              const int64_t* d_offsets, int32_t E, int64_t M,
                              const void* w, const uint8_t* w_scales, int64_t N,
@@ -484,7 +508,7 @@ mx_status grouped_linear_fwd(int32_t dtype, const void* x, const uint8_t* x_scal
                     E, (long long)M, (long long)N, (long long)K);
     if (!aligned(x, 16) || !aligned(w, 16))
         return fail(MX_ERR_INVALID_ARG, "grouped_linear_fwd: x and w must be 16-byte aligned");
-    if (dtype == MX_DTYPE_BF16 || dtype == MX_DTYPE_MXFP8) {
+    if (dtype >= MX_DTYPE_BF16 && dtype <= MX_DTYPE_MXFP8_MXFP4) {
         const mx_status cs = check_device_offsets("grouped_linear_fwd", d_offsets, E, M, true, s);
         if (cs != MX_OK) return cs;
     }
@@ -505,6 +529,9 @@ mx_status grouped_linear_fwd(int32_t dtype, const void* x, const uint8_t* x_scal
                               }),
                         "bf16_grouped");
     }
+    if (dtype == MX_DTYPE_MXFP4 || dtype == MX_DTYPE_MXFP8_MXFP4)
+        return linear_mxfp4(dtype == MX_DTYPE_MXFP4, x, x_scales, d_offsets, E, M, w, w_scales, N, K,
+                            d_row_scale, y, s);
     if (dtype != MX_DTYPE_MXFP8)
         return fail(MX_ERR_INVALID_ARG, "grouped_linear_fwd: unknown dtype %d", dtype);
     if (!x_scales || !w_scales)
@@ -1171,6 +1198,98 @@ mx_status moe_combine_bwd(const void* dout, int64_t T, int64_t H, int32_t k,
                                   static_cast<uint16_t*>(dy), d_dw, s);
                           }),
                     "combine_bwd");
+}
+
+// ---- the MoE layer for a few tokens ----------------------------------------------
+namespace {
+struct LayerWs {
+    size_t n_act, act, tok, r, xq, xqs, z, zs, total;
+};
+LayerWs layer_ws(int32_t wdtype, int64_t T, int32_t E, int32_t k, int64_t H, int64_t F) {
+    const bool mxw = wdtype != MX_DTYPE_BF16;
+    const int64_t rows = T * k;
+    Carver c;
+    LayerWs L{};
+    L.n_act = c.take(4);
+    L.act = c.take((size_t)(rows < E ? rows : E) * 16);
+    L.tok = c.take((size_t)rows * 4);
+    L.r = c.take((size_t)rows * 4);
+    L.xq = c.take(mxw ? (size_t)(T * H) : 0);
+    L.xqs = c.take(mxw ? (size_t)(T * H / 32) : 0);
+    L.z = c.take((size_t)(rows * F) * (mxw ? 1 : 2));
+    L.zs = c.take(mxw ? (size_t)(rows * F / 32) : 0);
+    L.total = c.off;
+    return L;
+}
+mx_status check_layer_sizes(int32_t wdtype, int64_t T, int32_t E, int32_t k, int64_t H, int64_t F) {
+    if (wdtype != MX_DTYPE_BF16 && wdtype != MX_DTYPE_MXFP8 && wdtype != MX_DTYPE_MXFP4)
+        return fail(MX_ERR_INVALID_ARG, "moe_layer_fwd: unknown weight dtype %d", wdtype);
+    if (T < 0 || E < 1 || k < 1 || k > E || H <= 0 || F <= 0)
+        return fail(MX_ERR_INVALID_ARG, "moe_layer_fwd: bad sizes T=%lld E=%d k=%d H=%lld F=%lld",
+                    (long long)T, E, k, (long long)H, (long long)F);
+    if (T > MX_LAYER_MAX_TOKENS)
+        return fail(MX_ERR_UNSUPPORTED, "moe_layer_fwd: T=%lld exceeds %d tokens", (long long)T,
+                    MX_LAYER_MAX_TOKENS);
+    if (E > mx::kMaxGroups || k > 64)
+        return fail(MX_ERR_UNSUPPORTED, "moe_layer_fwd: E=%d, k=%d exceed %d experts or 64 slots", E, k,
+                    mx::kMaxGroups);
+    if (H % 128 || F % 128 || H > (1 << 24) || F > (1 << 24))
+        return fail(MX_ERR_UNSUPPORTED,
+                    "moe_layer_fwd: H=%lld and F=%lld must be multiples of 128 up to 2^24",
+                    (long long)H, (long long)F);
+    return MX_OK;
+}
+static_assert(MX_LAYER_MAX_TOKENS == mx::kLayerMaxTokens, "one bound");
+}  // namespace
+
+size_t moe_layer_ws_bytes(int32_t wdtype, int64_t T, int32_t E, int32_t k, int64_t H, int64_t F) {
+    if (check_layer_sizes(wdtype, T, E, k, H, F) != MX_OK) return 0;
+    return layer_ws(wdtype, T, E, k, H, F).total;
+}
+
+mx_status moe_layer_fwd(int32_t wdtype, const void* x, const float* d_logits, int64_t T, int32_t E,
+                        int32_t k, int64_t H, int64_t F, const void* w1, const uint8_t* w1_scales,
+                        const void* w2, const uint8_t* w2_scales, void* out, void* ws,
+                        size_t ws_bytes, mx_stream_t stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const mx_status st = check_layer_sizes(wdtype, T, E, k, H, F);
+    if (st != MX_OK) return st;
+    if (T == 0) return ok();
+    const bool mxw = wdtype != MX_DTYPE_BF16;
+    if (!x || !d_logits || !w1 || !w2 || !out || !ws)
+        return fail(MX_ERR_INVALID_ARG, "moe_layer_fwd: NULL argument");
+    if (mxw != (w1_scales != nullptr) || mxw != (w2_scales != nullptr))
+        return fail(MX_ERR_INVALID_ARG, "moe_layer_fwd: MX weights need scales, bf16 weights take none");
+    if (!aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(out, 16) ||
+        !aligned(d_logits, 4) || !aligned(w1_scales, 4) || !aligned(w2_scales, 4))
+        return fail(MX_ERR_INVALID_ARG,
+                    "moe_layer_fwd: x, w1, w2 and out must be 16-byte, scales and logits 4-byte aligned");
+    if (!aligned(ws, kAlign)) return fail(MX_ERR_INVALID_ARG, "moe_layer_fwd: ws must be 256-byte aligned");
+    const LayerWs L = layer_ws(wdtype, T, E, k, H, F);
+    if (ws_bytes < L.total)
+        return fail(MX_ERR_WORKSPACE, "moe_layer_fwd: ws has %zu bytes, needs %zu", ws_bytes, L.total);
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    mx::LayerArgs p{};
+    p.x = static_cast<const uint16_t*>(x);
+    p.logits = d_logits;
+    p.T = T; p.H = H; p.F = F; p.E = E; p.k = k;
+    p.w1 = static_cast<const uint8_t*>(w1);
+    p.w1s = w1_scales;
+    p.w2 = static_cast<const uint8_t*>(w2);
+    p.w2s = w2_scales;
+    p.out = static_cast<uint16_t*>(out);
+    p.plan = mx::LayerPlan{reinterpret_cast<int32_t*>(b + L.n_act), reinterpret_cast<int4*>(b + L.act),
+                           reinterpret_cast<int32_t*>(b + L.tok), reinterpret_cast<float*>(b + L.r)};
+    p.xq = b + L.xq;
+    p.xqs = b + L.xqs;
+    p.z = b + L.z;
+    p.zs = b + L.zs;
+    const mx::LayerWeights wf = wdtype == MX_DTYPE_BF16 ? mx::LayerWeights::kBf16
+                              : wdtype == MX_DTYPE_MXFP8 ? mx::LayerWeights::kMxfp8
+                                                         : mx::LayerWeights::kMxfp4;
+    return launched(timed("moe_layer", 6.0 * T * k * H * F, MX_WORK_FLOP, s,
+                          [&] { return mx::launch_layer(wf, p, s); }),
+                    "moe_layer");
 }
 
 mx_status mx_validate_offsets(const int64_t* h_offsets, int32_t G, int64_t M) {

@@ -181,6 +181,37 @@ hipError_t launch_dequant4(const uint8_t* codes, const uint8_t* scales, int64_t 
 hipError_t launch_quant4_cols(const uint16_t* x, int64_t batch, int64_t R, int64_t C, uint8_t* codes,
                               uint8_t* scales, hipStream_t s);
 
+// GroupedLinear on MXFP4 weights w [G][N][K/2] for few rows an expert: x
+// MXFP4 [M][K/2] (x_fp4) or MXFP8 [M][K] with row-major scales, K % 32 == 0,
+// N % 32 == 0, y bf16 [M][N].  Right for any M.
+hipError_t launch_linear4_few(bool x_fp4, const uint8_t* x, const uint8_t* xs, const int64_t* offs, int G,
+                              int64_t M, const uint8_t* w, const uint8_t* ws, int64_t N, int64_t K,
+                              const float* rscale, uint16_t* y, hipStream_t s);
+
+// ---- the MoE layer for a few tokens --------------------------------------------
+constexpr int kLayerMaxTokens = 128;
+enum class LayerWeights { kBf16, kMxfp8, kMxfp4 };
+// Routed rows sorted by (expert, token): n_act routed experts, act[a] =
+// {expert, first row, rows, 0}; token and routing weight of each row.
+struct LayerPlan {
+    int32_t* n_act;
+    int4* act;               // [min(E, T k)]
+    int32_t* tok;            // [T k]
+    float* r;                // [T k]
+};
+struct LayerArgs {
+    const uint16_t* x;       // [T][H]
+    const float* logits;     // [T][E]
+    int64_t T, H, F;
+    int E, k;
+    const uint8_t *w1, *w1s, *w2, *w2s;
+    uint16_t* out;           // [T][H]
+    LayerPlan plan;
+    uint8_t *xq, *xqs;       // MX weights: MXFP8 copy of x
+    uint8_t *z, *zs;         // [T k][F], MXFP8 (MX weights) or bf16
+};
+hipError_t launch_layer(LayerWeights wf, const LayerArgs& p, hipStream_t s);
+
 int device_cu_count();
 
 }  // namespace mx

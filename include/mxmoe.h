@@ -77,7 +77,12 @@ typedef enum {
     MX_ERR_LAUNCH = 4        /* a HIP launch or query failed */
 } mx_status;
 
-enum { MX_DTYPE_BF16 = 0, MX_DTYPE_MXFP8 = 1 };
+enum {
+    MX_DTYPE_BF16 = 0,
+    MX_DTYPE_MXFP8 = 1,
+    MX_DTYPE_MXFP4 = 2,        /* both operands of a product, or the weights of a layer */
+    MX_DTYPE_MXFP8_MXFP4 = 3   /* grouped_linear_fwd: x MXFP8, w MXFP4 */
+};
 enum { MX_TOKEN_ALIGN = 128, MX_BLOCK = 32 };
 
 /* Last error message of the calling thread ("" if none).  Never NULL. */
@@ -143,8 +148,21 @@ mx_status mxfp8_quantize(const void* x, int64_t batch, int64_t R, int64_t C,
  *                         in one device allocation made with hipMallocAsync
  *                         on `stream` and freed after the GEMM (a failed
  *                         allocation returns MX_ERR_LAUNCH).
+ *   dtype MX_DTYPE_MXFP4: x = packed E2M1 codes [M][K/2] with x_scales
+ *                         [M][K/32]; w = codes [E][N][K/2] with w_scales
+ *                         [E][N][K/32] (rowwise copies from mxfp4_quantize).
+ *   dtype MX_DTYPE_MXFP8_MXFP4: x as for MXFP8, w as for MXFP4.
+ *                         Both: K % 32 == 0, N % 32 == 0, K, N < 2^31; any M,
+ *                         with the faster kernels where K % 128 == 0.  Nothing
+ *                         is allocated.  A block with scale 255 makes the
+ *                         outputs it takes part in NaN.
  *   d_row_scale  fp32 [M] routing weight applied to each output row, or NULL.
  *   y            bf16 [M][N].
+ *
+ * The data gradient of a product with MXFP4 weights is the same call on the
+ * other copy of the weights: dX[rows of e] = dY[rows of e] . W[e], with
+ * dY [M][N] quantized rowwise as x, and mxfp4_quantize's columnwise copy
+ * (codes [E][K][N/2]) as w, N and K exchanged.
  */
 mx_status grouped_linear_fwd(int32_t dtype, const void* x,
                              const uint8_t* x_scales, const int64_t* d_offsets,
@@ -462,6 +480,42 @@ mx_status moe_combine(const void* y, int64_t M, int64_t H, const int32_t* d_row_
 mx_status moe_combine_bwd(const void* dout, int64_t T, int64_t H, int32_t k,
                           const int32_t* d_row_of, const float* d_w, const void* y,
                           int64_t M, void* dy, float* d_dw, mx_stream_t stream);
+
+/*
+ * moe_layer_fwd -- a whole MoE layer for a few tokens (decoding: each step
+ * brings one token per sequence, and the time goes into reading the routed
+ * experts' weights), inference only:
+ *   e_j, r_j  the k largest logits of a token and their softmax (as moe_router)
+ *   h_j = Q(x) . W1_e^T,   z_j = Q(r_j silu(h_j[:F]) h_j[F:])
+ *   out = sum over j of z_j . W2_e^T        (fp32; rounded once to bf16)
+ * with Q the MXFP8 block quantizer when the weights are MXFP8 or MXFP4 (the
+ * GroupedMLP's own operands), and for bf16 weights x as it is and z rounded to
+ * bf16.  One call replaces moe_router, moe_route_plan, moe_permute_quantize,
+ * the GroupedMLP forward and moe_combine, without quantizing weights; experts
+ * that no token picks are not read.  Three launches, no host
+ * synchronisation, one fixed order of every sum (two calls give the same bits).
+ *
+ *   wdtype    MX_DTYPE_BF16: w1 bf16 [E][2F][H], w2 bf16 [E][H][F], scales NULL.
+ *             MX_DTYPE_MXFP8, MX_DTYPE_MXFP4: rowwise copies of the same from
+ *             mxfp8_quantize / mxfp4_quantize with their scales.
+ *   x         bf16 [T][H];  d_logits fp32 [T][E];  out bf16 [T][H].
+ *   T <= MX_LAYER_MAX_TOKENS, 1 <= k <= min(E, 64), E <= 1024, H and F
+ *   multiples of 128 up to 2^24 (MX_ERR_UNSUPPORTED otherwise).
+ *   A logit of -inf (or NaN) masks its expert: it is not routed even if fewer
+ *   than k remain.  A token without a routed expert, such as a padding row with
+ *   every logit at -inf, gets a row of zeros and reads no weights.  A logit of
+ *   +inf makes its token's row NaN.  An infinity or a NaN in x makes that
+ *   token's row NaN (through the NaN scale of its block) and no other's.
+ *   ws        moe_layer_ws_bytes(..) bytes of scratch, 256-byte aligned, not
+ *             shared with a call that may run at the same time.
+ *   x, w1, w2 and out 16-byte aligned, scales and d_logits 4-byte aligned.
+ */
+#define MX_LAYER_MAX_TOKENS 128
+size_t moe_layer_ws_bytes(int32_t wdtype, int64_t T, int32_t E, int32_t k, int64_t H, int64_t F);
+mx_status moe_layer_fwd(int32_t wdtype, const void* x, const float* d_logits, int64_t T, int32_t E,
+                        int32_t k, int64_t H, int64_t F, const void* w1, const uint8_t* w1_scales,
+                        const void* w2, const uint8_t* w2_scales, void* out, void* ws,
+                        size_t ws_bytes, mx_stream_t stream);
 
 /*
  * Launch timing (diagnostics; not part of the computation).  Between

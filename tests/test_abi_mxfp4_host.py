@@ -57,3 +57,80 @@ def test_binding_refuses_host_tensors_and_wrong_types():
     q = gm.Mx4Tensor(torch.zeros((4, 16), dtype=torch.uint8), torch.zeros((4, 1), dtype=torch.uint8))
     with pytest.raises(ValueError, match="GPU"):
         gm.mxfp4_dequantize(q)
+
+
+FP4, FP8FP4, BF16, FP8 = gm.MX_DTYPE_MXFP4, gm.MX_DTYPE_MXFP8_MXFP4, gm.MX_DTYPE_BF16, gm.MX_DTYPE_MXFP8
+
+
+@pytest.mark.parametrize("dtype", [FP4, FP8FP4])
+@pytest.mark.parametrize("change,status,text", [
+    (dict(x=None), INVALID, "NULL"),
+    (dict(y=None), INVALID, "NULL"),
+    (dict(xs=None), INVALID, "scales"),
+    (dict(ws=None), INVALID, "scales"),
+    (dict(K=48), UNSUPPORTED, "K % 32"),
+    (dict(N=40), UNSUPPORTED, "N % 32"),
+    (dict(N=1 << 32), UNSUPPORTED, "too large"),
+    (dict(K=1 << 32), UNSUPPORTED, "too large"),
+    (dict(E=0), INVALID, "sizes"),
+    (dict(E=1025), INVALID, "sizes"),
+    (dict(M=-1), INVALID, "sizes"),
+    (dict(w=ODD), INVALID, "aligned"),
+    (dict(y=ODD), INVALID, "aligned"),
+    (dict(xs=ctypes.c_void_p(0x7f0000001002)), INVALID, "aligned"),
+])
+def test_linear_refusals(mxlib, dtype, change, status, text):
+    a = dict(x=P, xs=P, off=P, E=4, M=8, w=P, ws=P, N=64, K=64, r=None, y=P)
+    a.update(change)
+    assert mxlib.grouped_linear_fwd(dtype, *a.values(), None) == status
+    assert text in err(mxlib)
+
+
+def test_linear_unknown_dtype(mxlib):
+    for dtype in (-1, 4):
+        assert mxlib.grouped_linear_fwd(dtype, P, P, P, 4, 8, P, P, 64, 64, None, P, None) == INVALID
+        assert "dtype" in err(mxlib)
+
+
+@pytest.mark.parametrize("change,status,text", [
+    (dict(dtype=FP8FP4), INVALID, "dtype"),
+    (dict(T=-1), INVALID, "sizes"),
+    (dict(k=0), INVALID, "sizes"),
+    (dict(k=9), INVALID, "sizes"),
+    (dict(E=0), INVALID, "sizes"),
+    (dict(T=129), UNSUPPORTED, "tokens"),
+    (dict(E=1025), UNSUPPORTED, "experts"),
+    (dict(E=100, k=65), UNSUPPORTED, "slots"),
+    (dict(H=192), UNSUPPORTED, "multiples"),
+    (dict(F=96), UNSUPPORTED, "multiples"),
+    (dict(F=1 << 25), UNSUPPORTED, "multiples"),
+    (dict(x=None), INVALID, "NULL"),
+    (dict(logits=None), INVALID, "NULL"),
+    (dict(ws=None), INVALID, "NULL"),
+    (dict(s1=None), INVALID, "scales"),
+    (dict(dtype=BF16), INVALID, "scales"),
+    (dict(x=ODD), INVALID, "aligned"),
+    (dict(out=ODD), INVALID, "aligned"),
+    (dict(s2=ctypes.c_void_p(0x7f0000001001)), INVALID, "aligned"),
+    (dict(ws=ctypes.c_void_p(0x7f0000001010)), INVALID, "256-byte"),
+    (dict(n=100), WORKSPACE, "needs"),
+])
+def test_layer_refusals(mxlib, change, status, text):
+    a = dict(dtype=FP4, x=P, logits=P, T=4, E=8, k=2, H=256, F=256, w1=P, s1=P, w2=P, s2=P, out=P,
+             ws=P, n=1 << 30)
+    a.update(change)
+    assert mxlib.moe_layer_fwd(*a.values(), None) == status
+    assert text in err(mxlib)
+
+
+def test_layer_workspace_bytes(mxlib):
+    f = mxlib.moe_layer_ws_bytes
+    T, E, k, H, F = 64, 64, 8, 2048, 1408
+    need = T * H * 33 // 32 + T * k * F * 33 // 32 + T * k * 8 + E * 16
+    assert need <= f(FP4, T, E, k, H, F) <= need + 16 * 256
+    assert f(FP4, T, E, k, H, F) == f(FP8, T, E, k, H, F)
+    assert T * k * F * 2 <= f(BF16, T, E, k, H, F)
+    assert f(FP4, 0, E, k, H, F) > 0
+    assert f(FP4, 129, E, k, H, F) == 0 and f(FP8FP4, T, E, k, H, F) == 0
+    # the largest sizes do not overflow
+    assert f(BF16, 128, 1024, 64, 1 << 24, 1 << 24) > 128 * 64 * (1 << 25)
