@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxmoe.so")
 SOURCES = ["api.cpp", "quantize.hip", "gemm_mxfp8.hip", "gemm_bf16.hip", "route.hip",
-           "fp8_tensor.hip", "quantize_mxfp4.hip", "few_rows.hip"]
+           "fp8_tensor.hip", "quantize_mxfp4.hip", "few_rows.hip",
+           "gemm_mxfp4.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

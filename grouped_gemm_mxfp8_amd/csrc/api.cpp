@@ -485,12 +485,27 @@ static mx_status linear_mxfp4(bool x_fp4, const void* x, const uint8_t* x_scales
         return fail(MX_ERR_INVALID_ARG,
                     "grouped_linear_fwd: y must be 16-byte aligned and scales 4-byte aligned");
     if (M == 0) return ok();
+    const uint8_t *xc = static_cast<const uint8_t*>(x), *wc = static_cast<const uint8_t*>(w);
+    const int64_t xld = x_fp4 ? K / 2 : K;
+    const bool tiles_fit = K % 128 == 0 && 256 * xld <= kI32Max && N <= (1 << 27);
+    if (tiles_fit && M > (int64_t)64 * E) {
+        mx::GemmProblem p{};
+        p.offs = d_offsets;
+        p.G = E;
+        p.M = M; p.N = N; p.K = K;
+        p.A = mx::MxOperand{xc, x_scales, xld, 0};
+        p.B = mx::MxOperand{wc, w_scales, K / 2, N};
+        p.C = y; p.ldc = N;
+        p.rscale = d_row_scale;
+        return launched(timed("linear4_tile", 2.0 * M * N * K, MX_WORK_FLOP, s,
+                              [&] { return mx::launch_linear4_tile(x_fp4, p, s); }),
+                        "linear4_tile");
+    }
     return launched(timed("linear4_few", 2.0 * M * N * K, MX_WORK_FLOP, s,
                           [&] {
-                              return mx::launch_linear4_few(
-                                  x_fp4, static_cast<const uint8_t*>(x), x_scales, d_offsets, E, M,
-                                  static_cast<const uint8_t*>(w), w_scales, N, K, d_row_scale,
-                                  static_cast<uint16_t*>(y), s);
+                              return mx::launch_linear4_few(x_fp4, xc, x_scales, d_offsets, E, M, wc,
+                                                            w_scales, N, K, d_row_scale,
+                                                            static_cast<uint16_t*>(y), s);
                           }),
                     "linear4_few");
 }

@@ -188,6 +188,11 @@ hipError_t launch_linear4_few(bool x_fp4, const uint8_t* x, const uint8_t* xs, c
                               int64_t M, const uint8_t* w, const uint8_t* ws, int64_t N, int64_t K,
                               const float* rscale, uint16_t* y, hipStream_t s);
 
+// The same in 256 x 256 tiles: K % 128 == 0, 256 rows of an operand and of its
+// scales below 2^31 bytes, N <= 2^27.  p: offs, G, M, N, K, A (x), B (w), C,
+// ldc = N, rscale.
+hipError_t launch_linear4_tile(bool x_fp4, const GemmProblem& p, hipStream_t s);
+
 // ---- the MoE layer for a few tokens --------------------------------------------
 constexpr int kLayerMaxTokens = 128;
 enum class LayerWeights { kBf16, kMxfp8, kMxfp4 };

@@ -268,3 +268,18 @@ def test_mx_check_refuses_bad_offsets(dev, monkeypatch):
     for bad, msg in (([0, 9, 8], "decrease"), ([0, 4, 7], "row count"), ([1, 4, 8], "offsets[0]")):
         with pytest.raises(gm.MxError, match=re.escape(msg)):
             gm.grouped_linear_fwd(xq, torch.tensor(bad, dtype=torch.int64, device=dev), wq)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 1024])
+def test_more_tiles_than_workgroups(dev, K, fmt):
+    """324 and more tiles of 256 x 256 on 256 workgroups: each runs a chain
+    whose last K steps load the next tile's first ones; one to eight K steps,
+    whole and half ones, odd and even."""
+    xq, wq, off, offd, r = make([9000, 37, 0, 11000, 5], K, 1024 - 32, K, fmt, dev)
+    y = gm.grouped_linear_fwd(xq, offd, wq)
+    ys = gm.grouped_linear_fwd(xq, offd, wq, row_scale=r)
+    torch.cuda.synchronize()
+    x, w = values(xq), values(wq)
+    assert_close(y, x, w, off, fmt=fmt)
+    assert_close(ys, x, w, off, r, fmt=fmt)
