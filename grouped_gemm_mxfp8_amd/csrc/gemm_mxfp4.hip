@@ -227,53 +227,80 @@ linear4_tile_kernel(GemmProblem p) {
             };
 
             // ---- fragments ----
-            // lane (r16, q): row r16 of a block.  MXFP4 x: both operands' chunks
-            // 2q and 2q + 1 (32 values, one scale block each; MFMA h takes chunk
-            // 2q + h of every lane and scale byte 2q + h).  MXFP8 x: x chunks q
-            // and q + 4 (K values 16q.. and 64 + 16q..), w chunk q of its 64 bytes
-            // (values 32q..), scale byte q: the pairing of the mixed MFMA.
+            // lane (r16, q): row r16 of a block.  MXFP4 x: chunks 2q and 2q + 1 of
+            // both operands, 32 values (one scale block) each; the first MFMA takes
+            // the lower one of even q and the higher one of odd q, the second the
+            // other.  (A read cycle serves 16 lanes of two neighbouring q and 16
+            // rows: with the lower chunk for every q they met in the same banks,
+            // 12 % of the kernel's cycles.)   MXFP8 x: x chunks q and q + 4 (K values 16q.. and
+            // 64 + 16q..), w chunk q of its 64 bytes (values 32q..), scale byte q: the
+            // pairing of the mixed MFMA.
             v4i af[8][2], bf[8][F::kSub];
-            int asc[8], bsc[8];
+            int asc[8][F::kSub], bsc[8][F::kSub];
             const int swz = r16 & 7;
             const int a_row = wm * 128 + r16, b_row = wn * 128 + r16;
-            const int ac0 = XF4 ? 2 * q : q, ac1 = XF4 ? 2 * q + 1 : q + 4;
+            const int ac0 = XF4 ? 2 * q + (q & 1) : q, ac1 = XF4 ? 2 * q + 1 - (q & 1) : q + 4;
             const int a0 = a_row * 128 + ((ac0 ^ swz) << 4), a1 = a_row * 128 + ((ac1 ^ swz) << 4);
-            const int b0 = XF4 ? b_row * 128 + (((2 * q) ^ swz) << 4)
+            const int b0 = XF4 ? b_row * 128 + ((ac0 ^ swz) << 4)
                                : (b_row >> 1) * 128 + ((((r16 & 1) * 4 + q) ^ (r16 >> 1)) << 4);
-            const int b1 = b_row * 128 + (((2 * q + 1) ^ swz) << 4);
+            const int b1 = b_row * 128 + ((ac1 ^ swz) << 4);
+            // the scale bytes of those chunks (a_s1: MXFP4 only)
+            const int a_s0 = a_row * (4 * F::kSub) + (XF4 ? ac0 : q), a_s1 = a_row * (4 * F::kSub) + ac1;
+            const int b_s0 = b_row * (4 * F::kSub) + (XF4 ? ac0 : q), b_s1 = b_row * (4 * F::kSub) + ac1;
             auto read_a = [&](auto ic, int st) {
                 constexpr int i = decltype(ic)::value;
                 af[i][0] = *reinterpret_cast<const v4i*>(sm.a[st] + a0 + i * 2048);
                 af[i][1] = *reinterpret_cast<const v4i*>(sm.a[st] + a1 + i * 2048);
-                if constexpr (XF4) asc[i] = *reinterpret_cast<const uint16_t*>(sm.as[st] + (a_row + i * 16) * 8 + 2 * q);
-                else asc[i] = sm.as[st][(a_row + i * 16) * 4 + q];
+                asc[i][0] = sm.as[st][a_s0 + i * 64 * F::kSub];
+                if constexpr (XF4) asc[i][F::kSub - 1] = sm.as[st][a_s1 + i * 64 * F::kSub];
             };
             auto read_b = [&](auto jc, int st) {
                 constexpr int j = decltype(jc)::value;
                 bf[j][0] = *reinterpret_cast<const v4i*>(sm.b[st] + b0 + j * 16 * F::kWBytes);
+                bsc[j][0] = sm.bs[st][b_s0 + j * 64 * F::kSub];
                 if constexpr (XF4) {
                     bf[j][1] = *reinterpret_cast<const v4i*>(sm.b[st] + b1 + j * 2048);
-                    bsc[j] = *reinterpret_cast<const uint16_t*>(sm.bs[st] + (b_row + j * 16) * 8 + 2 * q);
-                } else {
-                    bsc[j] = sm.bs[st][(b_row + j * 16) * 4 + q];
+                    bsc[j][F::kSub - 1] = sm.bs[st][b_s1 + j * 64 * F::kSub];
                 }
             };
             v4f acc[8][8];
             auto wide = [](const v4i& x) { return v8i{x.x, x.y, x.z, x.w, 0, 0, 0, 0}; };
-            // FIRST: the accumulation starts from zero
-            auto mfma = [&](auto ic, auto jc, auto firstc) {
-                constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
-                const v4f c0 = decltype(firstc)::value ? v4f{0.f, 0.f, 0.f, 0.f} : acc[i][j];
+            // Slot t of a pass over rows i0 .. i0 + 3: column t / 4.  MXFP8 x: row
+            // t % 4.  MXFP4 x: two MFMAs, of rows 0 and 1 in slots 0 (first half of
+            // their 256 values) and 1 (second half), rows 2 and 3 in slots 2 and 3:
+            // the halves of a block follow each other at a distance of two, since
+            // an MFMA whose input is the previous one's output would wait for it.
+            // FIRST: the accumulation starts from zero.
+            auto mfma = [&](auto tc, auto i0c, auto firstc) {
+                constexpr int t = decltype(tc)::value, j = t / 4, i0 = decltype(i0c)::value;
                 if constexpr (XF4) {
-                    const v4f c1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        wide(bf[j][0]), wide(af[i][0]), c0, 4, 4, 0, bsc[j], 0, asc[i]);
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        wide(bf[j][F::kSub - 1]), wide(af[i][1]), c1, 4, 4, 1, bsc[j], 1, asc[i]);
+                    constexpr int h = t & 1, i = i0 + (t & 2);
+                    static_for<2>([&](auto dc) {
+                        constexpr int r = i + decltype(dc)::value;
+                        const v4f c = decltype(firstc)::value && h == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : acc[r][j];
+                        acc[r][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            wide(bf[j][h * (F::kSub - 1)]), wide(af[r][h]), c, 4, 4, 0, bsc[j][h * (F::kSub - 1)], 0,
+                            asc[r][h * (F::kSub - 1)]);
+                    });
                 } else {
+                    constexpr int i = i0 + t % 4;
                     const v8i x{af[i][0].x, af[i][0].y, af[i][0].z, af[i][0].w,
                                 af[i][1].x, af[i][1].y, af[i][1].z, af[i][1].w};
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(bf[j][0]), x, c0, 4, 0, 0,
-                                                                                 bsc[j], 0, asc[i]);
+                    const v4f c = decltype(firstc)::value ? v4f{0.f, 0.f, 0.f, 0.f} : acc[i][j];
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(bf[j][0]), x, c, 4, 0, 0,
+                                                                                 bsc[j][0], 0, asc[i][0]);
+                }
+            };
+            // The accumulators take all 256 AGPRs.  Held there between the steps,
+            // each MXFP4 block keeps its registers through its two MFMAs; left to
+            // itself the compiler gave the first one's result others and moved some
+            // 130 registers a step.
+            auto pin = [&]() {
+                if constexpr (XF4) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));
                 }
             };
             // K step ks with the loads of step kl of s into the stage it frees.
@@ -287,7 +314,7 @@ linear4_tile_kernel(GemmProblem p) {
                 lds_barrier();
                 static_for<32>([&](auto sc) {
                     constexpr int t = decltype(sc)::value;
-                    mfma(std::integral_constant<int, t % 4>{}, std::integral_constant<int, t / 4>{}, firstc);
+                    mfma(sc, std::integral_constant<int, 0>{}, firstc);
                     __builtin_amdgcn_sched_barrier(0);
                     constexpr int u = load_at_a<XF4>(t);
                     if constexpr (u >= 0) dma(std::integral_constant<int, u>{}, livec, s, cur, kl);
@@ -296,11 +323,16 @@ linear4_tile_kernel(GemmProblem p) {
                 wait_vm<F::kNA>();
                 lds_barrier();
                 static_for<32>([&](auto sc) {
-                    constexpr int t = decltype(sc)::value, j = t / 4, i = 4 + t % 4;
-                    mfma(std::integral_constant<int, i>{}, std::integral_constant<int, j>{}, firstc);
+                    constexpr int t = decltype(sc)::value, j = t / 4;
+                    mfma(sc, std::integral_constant<int, 4>{}, firstc);
                     __builtin_amdgcn_sched_barrier(0);
                     if constexpr (t < 4) read_a(std::integral_constant<int, t>{}, nxt);
-                    if constexpr (t >= 28) read_a(std::integral_constant<int, i>{}, nxt);
+                    // in the last column a row is read once its last MFMA has issued
+                    if constexpr (t >= 28 && !XF4) read_a(std::integral_constant<int, 4 + t % 4>{}, nxt);
+                    if constexpr (t >= 28 && XF4 && t % 2 == 1) {
+                        read_a(std::integral_constant<int, 4 + (t & 2)>{}, nxt);
+                        read_a(std::integral_constant<int, 5 + (t & 2)>{}, nxt);
+                    }
                     if constexpr (t % 4 == 3) read_b(std::integral_constant<int, j>{}, nxt);
                     constexpr int u = load_at_b<XF4>(t);
                     if constexpr (u >= 0) dma(std::integral_constant<int, u>{}, livec, s, cur, kl);
@@ -340,7 +372,11 @@ linear4_tile_kernel(GemmProblem p) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
             }
-            for (; ks + 2 < nk; ++ks) step(ks, std::true_type{}, own, ks + 2, std::false_type{});
+            for (; ks + 2 < nk; ++ks) {
+                pin();
+                step(ks, std::true_type{}, own, ks + 2, std::false_type{});
+                pin();
+            }
             Loc Ln = L;
             Src nx = own;
             nx.nk = 0;                             // no next tile: zero-range loads
@@ -348,7 +384,11 @@ linear4_tile_kernel(GemmProblem p) {
                 Ln = locate(wnext);
                 nx = src_of(Ln);
             }
-            for (; ks < nk; ++ks) step(ks, std::false_type{}, nx, ks + 2 - nk, std::false_type{});
+            for (; ks < nk; ++ks) {
+                pin();
+                step(ks, std::false_type{}, nx, ks + 2 - nk, std::false_type{});
+                pin();
+            }
             store_tile_bf16_regs<SCALED>(acc, p, L.g, L.m0, L.mvalid, L.n0, wm, wn, lane_now(), 1.0f,
                                          SCALED ? &s_rsw[wave * 128] : nullptr);
             if (!has_next) break;
