@@ -31,18 +31,32 @@ struct Fmt {
     static constexpr int kBK = XF4 ? 256 : 128;          // values
     static constexpr int kSub = XF4 ? 2 : 1;             // MFMAs deep
     static constexpr int kWBytes = kBK / 2;              // bytes of a weight row
-    static constexpr int kALoads = 8, kBLoads = kWBytes / 16, kSLoads = kSub;   // per wave
-    static constexpr int kLoads = kALoads + kBLoads + 2 * kSLoads;
-    // loads issued in a step's first pass (rows 0..3), the rest in the second
-    static constexpr int kNA = XF4 ? 13 : 9;
+    static constexpr int kALoads = 8, kBLoads = kWBytes / 16;   // code loads per wave
+    static constexpr int kCodeLoads = kALoads + kBLoads;
+    // block scales of a row and step: kSub dwords.  Loaded a step at a time
+    // (4 bytes a lane), or (WIN) 16 bytes of a row at a time, a window of kWin
+    // steps: a load instruction then asks for its 64 rows' lines half or a
+    // quarter as often, and those requests were as many as the codes'.
+    static constexpr int kWin = 4 / kSub;
+    // loads issued in a step's first pass (rows 0..3); the rest, the scales
+    // among them, in the second
+    static constexpr int kNA = XF4 ? 11 : 8;
+};
+template <bool XF4, bool WIN>
+struct Loads {
+    using F = Fmt<XF4>;
+    static constexpr int kScale = WIN ? 1 : F::kSub;            // per wave and operand
+    static constexpr int kAll = F::kCodeLoads + 2 * kScale;
 };
 
-template <bool XF4>
+template <bool XF4, bool WIN>
 struct Smem {
+    static constexpr int kSRow = WIN ? 16 : 4 * Fmt<XF4>::kSub;   // scale bytes kept of a row
     uint8_t a[2][BM * 128];
     uint8_t b[2][BN * Fmt<XF4>::kWBytes];
-    uint8_t as[2][BM * 4 * Fmt<XF4>::kSub];     // a row's block scales of the step
-    uint8_t bs[2][BN * 4 * Fmt<XF4>::kSub];
+    uint8_t as[2][BM * kSRow];                 // by step, or by window
+    uint8_t bs[2][BN * kSRow];
+    uint8_t none[WIN ? 1024 : 16];             // where a load of no bytes writes its zeros
 };
 
 // Slot after which load u of a pass of n loads is issued, over slots
@@ -55,20 +69,22 @@ constexpr int load_at_a(int s) {
     return -1;
 }
 // (the second pass reads the next step's fragments in its first and last slots)
-template <bool XF4>
+template <bool XF4, bool WIN>
 constexpr int load_at_b(int s) {
-    constexpr int n = Fmt<XF4>::kLoads - Fmt<XF4>::kNA;
+    constexpr int n = Loads<XF4, WIN>::kAll - Fmt<XF4>::kNA;
     for (int u = 0; u < n; ++u)
         if (slot_of(u, n, 4, 23) == s) return Fmt<XF4>::kNA + u;
     return -1;
 }
-template <bool XF4>
+template <bool XF4, bool WIN>
 constexpr bool loads_covered() {
     int n = 0;
-    for (int s = 0; s < 32; ++s) n += (load_at_a<XF4>(s) >= 0) + (load_at_b<XF4>(s) >= 0);
-    return n == Fmt<XF4>::kLoads;
+    for (int s = 0; s < 32; ++s) n += (load_at_a<XF4>(s) >= 0) + (load_at_b<XF4, WIN>(s) >= 0);
+    return n == Loads<XF4, WIN>::kAll && Fmt<XF4>::kNA <= Fmt<XF4>::kCodeLoads;
 }
-static_assert(loads_covered<true>() && loads_covered<false>(), "every load has a slot of its own");
+static_assert(loads_covered<true, true>() && loads_covered<false, true>() && loads_covered<true, false>() &&
+                  loads_covered<false, false>(),
+              "every load has a slot of its own, the scales' in the second pass");
 
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -87,14 +103,17 @@ struct Loc {
 };
 
 // HALF: K % 256 == 128 (MXFP4): the last step holds 128 values; its chunks 4..7
-// and their scales are read past the descriptors' ranges, as zeros.
+// are read past the descriptors' ranges, as zeros, and their scales as 0.
+// WIN: scales in windows of 16 bytes, K >= 512 (a row has 16 of them).
 // SCALED: row scales.
-template <bool XF4, bool HALF, bool SCALED>
+template <bool XF4, bool HALF, bool WIN, bool SCALED>
 __global__ void __launch_bounds__(NT4, 1)
 linear4_tile_kernel(GemmProblem p) {
     using F = Fmt<XF4>;
+    using LD = Loads<XF4, WIN>;
+    using SM = Smem<XF4, WIN>;
     static_assert(!HALF || XF4, "an MXFP8 step is 128 values");
-    __shared__ __attribute__((aligned(16))) Smem<XF4> sm;
+    __shared__ __attribute__((aligned(16))) SM sm;
     __shared__ int s_prefix[kMaxGroups + 1];
     __shared__ int64_t s_offs[kMaxGroups + 1];   // no global load while the chain's are in flight
     __shared__ float s_rsw[SCALED ? 4 * 128 : 1];
@@ -174,7 +193,8 @@ linear4_tile_kernel(GemmProblem p) {
         int w = slot;
         Loc L = locate(w);
         bool pre = false;
-        int base = 0;
+        int base = 0;          // stage of the tile's step 0
+        int sbase = 0;         // and scale buffer of its window 0
         for (;;) {
             const int wnext = w + grid;
             const bool has_next = wnext < total;
@@ -193,36 +213,52 @@ linear4_tile_kernel(GemmProblem p) {
             const uint32_t boff =
                 XF4 ? (uint32_t)((wave * 64 + lrow) * ldb + lchunk * 16)
                     : (uint32_t)((wave * 64 + lrow * 2 + (lchunk >> 2)) * ldb + (lchunk & 3) * 16);
-            // scales: lane l of load t fetches 4 bytes of row (t * 64 + l) / kSub
-            const uint32_t soff = XF4 ? (uint32_t)((wave * 64 + (lane >> 1)) * lds + (lane & 1) * 4)
-                                      : (uint32_t)((wave * 64 + lane) * lds);
+            // scales: a window's 16 bytes of row wave * 64 + l; a step's kSub dwords:
+            // lane l of load t fetches 4 bytes of row (t * 64 + l) / kSub
+            const uint32_t soff = !WIN && XF4 ? (uint32_t)((wave * 64 + (lane >> 1)) * lds + (lane & 1) * 4)
+                                              : (uint32_t)((wave * 64 + lane) * lds);
             const uint32_t over_c = HALF && lchunk >= 4 ? 0x80000000u : 0u;
             const uint32_t over_s = HALF && (lane & 1) ? 0x80000000u : 0u;
-            // load u of step ks of a tile into stage st; LIVE: ks < nk is known
-            auto dma = [&](auto uc, auto livec, const Src& s, int st, int ks) {
+            // first scale byte of a step's window in its row: the last window ends
+            // with the row
+            auto win_byte = [&](int ks) {
+                return min((uint32_t)(ks / F::kWin) * 16u, (uint32_t)lds - 16u);
+            };
+            // load u of step ks of a tile into stage st, scales into their buffer sb
+            // (WIN: those of the window that starts at ks, if one does); LIVE: ks < nk is known
+            auto dma = [&](auto uc, auto livec, const Src& s, int st, int sb, int ks) {
                 constexpr int u = decltype(uc)::value;
                 const bool live = decltype(livec)::value || ks < s.nk;
                 const bool last = HALF && ks + 1 == s.nk;
                 const uint32_t oc = HALF && last ? over_c : 0u, os = HALF && last ? over_s : 0u;
                 auto rng = [&](const v4i& r) { return live ? r : v4i{r.x, r.y, 0, r.w}; };
                 if constexpr (u < F::kALoads) {
-                    dma_b128<u * 1024>(rng(s.ra), smb + (uint32_t)offsetof(Smem<XF4>, a) + st * (BM * 128) + wave * 8192,
+                    dma_b128<u * 1024>(rng(s.ra), smb + (uint32_t)offsetof(SM, a) + st * (BM * 128) + wave * 8192,
                                        (aoff + (uint32_t)(u * 8 * lda)) | oc, (uint32_t)ks * 128u);
                 } else if constexpr (u < F::kALoads + F::kBLoads) {
                     constexpr int v = u - F::kALoads;
                     dma_b128<v * 1024>(rng(s.rb),
-                                       smb + (uint32_t)offsetof(Smem<XF4>, b) + st * (BN * F::kWBytes) +
+                                       smb + (uint32_t)offsetof(SM, b) + st * (BN * F::kWBytes) +
                                            wave * (F::kBLoads * 1024),
                                        (boff + (uint32_t)(v * (XF4 ? 8 : 16) * ldb)) | oc,
                                        (uint32_t)ks * (uint32_t)F::kWBytes);
                 } else {
-                    constexpr int v = u - F::kALoads - F::kBLoads;       // x scales, then w scales
-                    constexpr bool isx = v < F::kSLoads;
-                    constexpr int t = isx ? v : v - F::kSLoads;
-                    dma_b32<t * 256>(rng(isx ? s.rsa : s.rsb),
-                                     smb + (uint32_t)(isx ? offsetof(Smem<XF4>, as) : offsetof(Smem<XF4>, bs)) +
-                                         st * (BM * 4 * F::kSub) + wave * (256 * F::kSub),
-                                     (soff + (uint32_t)(t * 32 * lds)) | os, (uint32_t)ks * (4u * F::kSub));
+                    constexpr int v = u - F::kCodeLoads;       // x scales, then w scales
+                    constexpr bool isx = v < LD::kScale;
+                    constexpr int t = isx ? v : v - LD::kScale;
+                    const v4i r = rng(isx ? s.rsa : s.rsb);
+                    const uint32_t at = smb + (uint32_t)(isx ? offsetof(SM, as) : offsetof(SM, bs));
+                    if constexpr (WIN) {
+                        // between window starts a load of no bytes, so that every step
+                        // issues the same instructions
+                        const bool start = ks % F::kWin == 0;
+                        dma_b128(start ? r : v4i{r.x, r.y, 0, r.w},
+                                 start ? at + sb * (BM * 16) + wave * 1024 : smb + (uint32_t)offsetof(SM, none),
+                                 soff, win_byte(ks));
+                    } else {
+                        dma_b32<t * 256>(r, at + st * (BM * SM::kSRow) + wave * (256 * F::kSub),
+                                         (soff + (uint32_t)(t * 32 * lds)) | os, (uint32_t)ks * (4u * F::kSub));
+                    }
                 }
             };
 
@@ -244,24 +280,48 @@ linear4_tile_kernel(GemmProblem p) {
             const int b0 = XF4 ? b_row * 128 + ((ac0 ^ swz) << 4)
                                : (b_row >> 1) * 128 + ((((r16 & 1) * 4 + q) ^ (r16 >> 1)) << 4);
             const int b1 = b_row * 128 + ((ac1 ^ swz) << 4);
-            // the scale bytes of those chunks (a_s1: MXFP4 only)
-            const int a_s0 = a_row * (4 * F::kSub) + (XF4 ? ac0 : q), a_s1 = a_row * (4 * F::kSub) + ac1;
-            const int b_s0 = b_row * (4 * F::kSub) + (XF4 ? ac0 : q), b_s1 = b_row * (4 * F::kSub) + ac1;
-            auto read_a = [&](auto ic, int st) {
-                constexpr int i = decltype(ic)::value;
-                af[i][0] = *reinterpret_cast<const v4i*>(sm.a[st] + a0 + i * 2048);
-                af[i][1] = *reinterpret_cast<const v4i*>(sm.a[st] + a1 + i * 2048);
-                asc[i][0] = sm.as[st][a_s0 + i * 64 * F::kSub];
-                if constexpr (XF4) asc[i][F::kSub - 1] = sm.as[st][a_s1 + i * 64 * F::kSub];
+            // scale bytes of those chunks: byte of the row's kept ones, from the
+            // step's first (a_s1, b_s1: MXFP4 only)
+            const int a_s0 = a_row * SM::kSRow + (XF4 ? ac0 : q), a_s1 = a_row * SM::kSRow + ac1;
+            const int b_s0 = b_row * SM::kSRow + (XF4 ? ac0 : q), b_s1 = b_row * SM::kSRow + ac1;
+            // where a step's fragments lie: its stage, and the offset of its scales
+            struct Place {
+                int st, s;
             };
-            auto read_b = [&](auto jc, int st) {
+            auto place = [&](int ks) -> Place {
+                const int st = (base + ks) & 1;
+                if constexpr (WIN)
+                    return Place{st, ((sbase + ks / F::kWin) & 1) * (BM * SM::kSRow) +
+                                         (int)((uint32_t)ks * (4u * F::kSub) - win_byte(ks))};
+                else
+                    return Place{st, st * (BM * SM::kSRow)};
+            };
+            auto read_a = [&](auto ic, const Place& p) {
+                constexpr int i = decltype(ic)::value;
+                af[i][0] = *reinterpret_cast<const v4i*>(sm.a[p.st] + a0 + i * 2048);
+                af[i][1] = *reinterpret_cast<const v4i*>(sm.a[p.st] + a1 + i * 2048);
+                asc[i][0] = sm.as[0][p.s + a_s0 + i * 16 * SM::kSRow];
+                if constexpr (XF4) asc[i][F::kSub - 1] = sm.as[0][p.s + a_s1 + i * 16 * SM::kSRow];
+            };
+            auto read_b = [&](auto jc, const Place& p) {
                 constexpr int j = decltype(jc)::value;
-                bf[j][0] = *reinterpret_cast<const v4i*>(sm.b[st] + b0 + j * 16 * F::kWBytes);
-                bsc[j][0] = sm.bs[st][b_s0 + j * 64 * F::kSub];
+                bf[j][0] = *reinterpret_cast<const v4i*>(sm.b[p.st] + b0 + j * 16 * F::kWBytes);
+                bsc[j][0] = sm.bs[0][p.s + b_s0 + j * 16 * SM::kSRow];
                 if constexpr (XF4) {
-                    bf[j][1] = *reinterpret_cast<const v4i*>(sm.b[st] + b1 + j * 2048);
-                    bsc[j][F::kSub - 1] = sm.bs[st][b_s1 + j * 64 * F::kSub];
+                    bf[j][1] = *reinterpret_cast<const v4i*>(sm.b[p.st] + b1 + j * 2048);
+                    bsc[j][F::kSub - 1] = sm.bs[0][p.s + b_s1 + j * 16 * SM::kSRow];
                 }
+            };
+            // (WIN, HALF) the scale bytes read for chunks past K are some other
+            // row's: zero them before the last step's MFMAs
+            auto cut_scales = [&](int keep) {          // 0 or ~0
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int h = 0; h < F::kSub; ++h) {
+                        asc[i][h] &= keep;
+                        bsc[i][h] &= keep;
+                    }
             };
             v4f acc[8][8];
             auto wide = [](const v4i& x) { return v8i{x.x, x.y, x.z, x.w, 0, 0, 0, 0}; };
@@ -309,19 +369,22 @@ linear4_tile_kernel(GemmProblem p) {
             // landed (only the first pass's newer ones may be in flight), and after
             // the barrier everybody's: the second pass (rows 4..7) reads the next
             // fragments into the registers its MFMAs free.
-            auto step = [&](int ks, auto livec, const Src& s, int kl, auto firstc) {
-                const int cur = (base + ks) & 1, nxt = cur ^ 1;
+            // sb: the scale buffer for the window that starts at step kl of s.
+            auto step = [&](int ks, auto livec, const Src& s, int sb, int kl, auto firstc) {
+                const int cur = (base + ks) & 1;
                 lds_barrier();
+                if constexpr (WIN && HALF) cut_scales(ks + 1 == nk && q >= 2 ? 0 : ~0);
                 static_for<32>([&](auto sc) {
                     constexpr int t = decltype(sc)::value;
                     mfma(sc, std::integral_constant<int, 0>{}, firstc);
                     __builtin_amdgcn_sched_barrier(0);
                     constexpr int u = load_at_a<XF4>(t);
-                    if constexpr (u >= 0) dma(std::integral_constant<int, u>{}, livec, s, cur, kl);
+                    if constexpr (u >= 0) dma(std::integral_constant<int, u>{}, livec, s, cur, sb, kl);
                     __builtin_amdgcn_sched_barrier(0);
                 });
                 wait_vm<F::kNA>();
                 lds_barrier();
+                const Place nxt = place(ks + 1);
                 static_for<32>([&](auto sc) {
                     constexpr int t = decltype(sc)::value, j = t / 4;
                     mfma(sc, std::integral_constant<int, 4>{}, firstc);
@@ -334,8 +397,8 @@ linear4_tile_kernel(GemmProblem p) {
                         read_a(std::integral_constant<int, 5 + (t & 2)>{}, nxt);
                     }
                     if constexpr (t % 4 == 3) read_b(std::integral_constant<int, j>{}, nxt);
-                    constexpr int u = load_at_b<XF4>(t);
-                    if constexpr (u >= 0) dma(std::integral_constant<int, u>{}, livec, s, cur, kl);
+                    constexpr int u = load_at_b<XF4, WIN>(t);
+                    if constexpr (u >= 0) dma(std::integral_constant<int, u>{}, livec, s, cur, sb, kl);
                     __builtin_amdgcn_sched_barrier(0);
                 });
             };
@@ -355,16 +418,19 @@ linear4_tile_kernel(GemmProblem p) {
                 dma_b32(rr, la + 256u, (uint32_t)lane * 4u + 256u, 0u);
             }
             if (!pre) {
-                static_for<F::kLoads>([&](auto uc) { dma(uc, std::false_type{}, own, base, 0); });
-                static_for<F::kLoads>([&](auto uc) { dma(uc, std::false_type{}, own, base ^ 1, 1); });
-                wait_vm<F::kLoads>();
+                static_for<LD::kAll>([&](auto uc) { dma(uc, std::false_type{}, own, base, sbase, 0); });
+                static_for<LD::kAll>([&](auto uc) { dma(uc, std::false_type{}, own, base ^ 1, sbase, 1); });
+                wait_vm<LD::kAll>();
                 lds_barrier();
             }
-            static_for<8>([&](auto ic) { read_a(ic, base); });
-            static_for<8>([&](auto jc) { read_b(jc, base); });
+            const Place first = place(0);
+            static_for<8>([&](auto ic) { read_a(ic, first); });
+            static_for<8>([&](auto jc) { read_b(jc, first); });
+            auto buf = [&](int ks) { return WIN ? (sbase + ks / F::kWin) & 1 : 0; };
+            const int snext = WIN ? (sbase + (nk + F::kWin - 1) / F::kWin) & 1 : 0;   // the next tile's
             int ks = 0;
             if (nk >= 3) {
-                step(0, std::true_type{}, own, 2, std::true_type{});
+                step(0, std::true_type{}, own, buf(2), 2, std::true_type{});
                 ks = 1;
             } else {
 #pragma unroll
@@ -374,7 +440,7 @@ linear4_tile_kernel(GemmProblem p) {
             }
             for (; ks + 2 < nk; ++ks) {
                 pin();
-                step(ks, std::true_type{}, own, ks + 2, std::false_type{});
+                step(ks, std::true_type{}, own, buf(ks + 2), ks + 2, std::false_type{});
                 pin();
             }
             Loc Ln = L;
@@ -386,7 +452,7 @@ linear4_tile_kernel(GemmProblem p) {
             }
             for (; ks < nk; ++ks) {
                 pin();
-                step(ks, std::false_type{}, nx, ks + 2 - nk, std::false_type{});
+                step(ks, std::false_type{}, nx, snext, ks + 2 - nk, std::false_type{});
                 pin();
             }
             store_tile_bf16_regs<SCALED>(acc, p, L.g, L.m0, L.mvalid, L.n0, wm, wn, lane_now(), 1.0f,
@@ -394,6 +460,7 @@ linear4_tile_kernel(GemmProblem p) {
             if (!has_next) break;
             pre = nk >= 2;                         // a one-step tile loads nothing ahead
             base = uni(pre ? (base + nk) & 1 : 0);
+            sbase = uni(pre ? snext : 0);
             w = wnext;
             L = Ln;
         }
@@ -402,10 +469,12 @@ linear4_tile_kernel(GemmProblem p) {
     wait_vm<0>();
 }
 
-template <bool XF4, bool HALF>
+template <bool XF4, bool HALF, bool WIN>
 void launch_tile(const GemmProblem& p, int grid, hipStream_t s) {
-    if (p.rscale) hipLaunchKernelGGL((linear4_tile_kernel<XF4, HALF, true>), dim3(grid), dim3(NT4), 0, s, p);
-    else hipLaunchKernelGGL((linear4_tile_kernel<XF4, HALF, false>), dim3(grid), dim3(NT4), 0, s, p);
+    if (p.rscale)
+        hipLaunchKernelGGL((linear4_tile_kernel<XF4, HALF, WIN, true>), dim3(grid), dim3(NT4), 0, s, p);
+    else
+        hipLaunchKernelGGL((linear4_tile_kernel<XF4, HALF, WIN, false>), dim3(grid), dim3(NT4), 0, s, p);
 }
 
 }  // namespace
@@ -413,9 +482,10 @@ void launch_tile(const GemmProblem& p, int grid, hipStream_t s) {
 hipError_t launch_linear4_tile(bool x_fp4, const GemmProblem& p, hipStream_t s) {
     int grid = device_cu_count();
     grid = grid < 8 ? 8 : grid / 8 * 8;
-    if (!x_fp4) launch_tile<false, false>(p, grid, s);
-    else if (p.K % 256) launch_tile<true, true>(p, grid, s);
-    else launch_tile<true, false>(p, grid, s);
+    const bool win = p.K >= 512, half = p.K % 256 != 0;
+    if (!x_fp4) win ? launch_tile<false, false, true>(p, grid, s) : launch_tile<false, false, false>(p, grid, s);
+    else if (half) win ? launch_tile<true, true, true>(p, grid, s) : launch_tile<true, true, false>(p, grid, s);
+    else win ? launch_tile<true, false, true>(p, grid, s) : launch_tile<true, false, false>(p, grid, s);
     return hipGetLastError();
 }
 
