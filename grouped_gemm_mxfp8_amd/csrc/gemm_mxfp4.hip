@@ -14,9 +14,12 @@
 // are 64 or 128 bytes of a step.
 //
 // LDS layout: 128-byte lines of eight 16-byte chunks, chunk c of line n stored
-// at c ^ (n & 7), so that the eight lanes of a fragment read's cycle touch
-// eight different chunks.  A line is one row (two rows where a step has 64
-// bytes of a row).
+// at c ^ (n & 7), or for MXFP4 x at c ^ (n & 7) ^ (n >> 3 & 1).  A line is one
+// row (two rows where a step has 64 bytes of a row).  A cycle of a fragment
+// read serves 16 lanes, those of two neighbouring q with eight rows each (0-3
+// and 12-15 of one, 4-11 of the other), over 64 banks: these orders put the 16
+// chunks that each format's lanes take on different banks (0 conflicts
+// counted; with the first order for MXFP4 x, 12 % of the kernel's cycles).
 #include "gemm_device.h"
 
 namespace mx {
@@ -210,6 +213,8 @@ linear4_tile_kernel(GemmProblem p) {
             // chunk l & 7 of line l >> 3.
             const int lrow = lane >> 3, lchunk = (lane & 7) ^ lrow;
             const uint32_t aoff = (uint32_t)((wave * 64 + lrow) * lda + lchunk * 16);
+            // MXFP4 x: rows 8..15 of each 16 (odd loads) have chunk lchunk ^ 1 there
+            const uint32_t flip = (lchunk & 1) ? (uint32_t)-16 : 16u;
             const uint32_t boff =
                 XF4 ? (uint32_t)((wave * 64 + lrow) * ldb + lchunk * 16)
                     : (uint32_t)((wave * 64 + lrow * 2 + (lchunk >> 2)) * ldb + (lchunk & 3) * 16);
@@ -234,13 +239,14 @@ linear4_tile_kernel(GemmProblem p) {
                 auto rng = [&](const v4i& r) { return live ? r : v4i{r.x, r.y, 0, r.w}; };
                 if constexpr (u < F::kALoads) {
                     dma_b128<u * 1024>(rng(s.ra), smb + (uint32_t)offsetof(SM, a) + st * (BM * 128) + wave * 8192,
-                                       (aoff + (uint32_t)(u * 8 * lda)) | oc, (uint32_t)ks * 128u);
+                                       (aoff + (uint32_t)(u * 8 * lda) + (XF4 && (u & 1) ? flip : 0u)) | oc,
+                                       (uint32_t)ks * 128u);
                 } else if constexpr (u < F::kALoads + F::kBLoads) {
                     constexpr int v = u - F::kALoads;
                     dma_b128<v * 1024>(rng(s.rb),
                                        smb + (uint32_t)offsetof(SM, b) + st * (BN * F::kWBytes) +
                                            wave * (F::kBLoads * 1024),
-                                       (boff + (uint32_t)(v * (XF4 ? 8 : 16) * ldb)) | oc,
+                                       (boff + (uint32_t)(v * (XF4 ? 8 : 16) * ldb) + (XF4 && (v & 1) ? flip : 0u)) | oc,
                                        (uint32_t)ks * (uint32_t)F::kWBytes);
                 } else {
                     constexpr int v = u - F::kCodeLoads;       // x scales, then w scales
@@ -264,26 +270,26 @@ linear4_tile_kernel(GemmProblem p) {
 
             // ---- fragments ----
             // lane (r16, q): row r16 of a block.  MXFP4 x: chunks 2q and 2q + 1 of
-            // both operands, 32 values (one scale block) each; the first MFMA takes
-            // the lower one of even q and the higher one of odd q, the second the
-            // other.  (A read cycle serves 16 lanes of two neighbouring q and 16
-            // rows: with the lower chunk for every q they met in the same banks,
-            // 12 % of the kernel's cycles.)   MXFP8 x: x chunks q and q + 4 (K values 16q.. and
-            // 64 + 16q..), w chunk q of its 64 bytes (values 32q..), scale byte q: the
-            // pairing of the mixed MFMA.
+            // both operands, 32 values (one scale block) each, MFMA h of a block
+            // taking chunk 2q + h of every lane and byte h of the lane's two scales.
+            // MXFP8 x: x chunks q and q + 4 (K values 16q.. and 64 + 16q..), w chunk q
+            // of its 64 bytes (values 32q..), scale byte q: the pairing of the mixed
+            // MFMA.
             v4i af[8][2], bf[8][F::kSub];
-            int asc[8][F::kSub], bsc[8][F::kSub];
-            const int swz = r16 & 7;
+            int asc[8], bsc[8];
+            const int swz = (r16 & 7) ^ (XF4 ? r16 >> 3 : 0);
             const int a_row = wm * 128 + r16, b_row = wn * 128 + r16;
-            const int ac0 = XF4 ? 2 * q + (q & 1) : q, ac1 = XF4 ? 2 * q + 1 - (q & 1) : q + 4;
+            const int ac0 = XF4 ? 2 * q : q, ac1 = XF4 ? 2 * q + 1 : q + 4;
             const int a0 = a_row * 128 + ((ac0 ^ swz) << 4), a1 = a_row * 128 + ((ac1 ^ swz) << 4);
             const int b0 = XF4 ? b_row * 128 + ((ac0 ^ swz) << 4)
                                : (b_row >> 1) * 128 + ((((r16 & 1) * 4 + q) ^ (r16 >> 1)) << 4);
             const int b1 = b_row * 128 + ((ac1 ^ swz) << 4);
-            // scale bytes of those chunks: byte of the row's kept ones, from the
-            // step's first (a_s1, b_s1: MXFP4 only)
-            const int a_s0 = a_row * SM::kSRow + (XF4 ? ac0 : q), a_s1 = a_row * SM::kSRow + ac1;
-            const int b_s0 = b_row * SM::kSRow + (XF4 ? ac0 : q), b_s1 = b_row * SM::kSRow + ac1;
+            // those chunks' scales among the row's kept ones, from the step's first
+            const int a_s = a_row * SM::kSRow + ac0, b_s = b_row * SM::kSRow + ac0;
+            auto scales = [](const uint8_t* s) -> int {
+                if constexpr (XF4) return *reinterpret_cast<const uint16_t*>(s);
+                else return *s;
+            };
             // where a step's fragments lie: its stage, and the offset of its scales
             struct Place {
                 int st, s;
@@ -300,28 +306,22 @@ linear4_tile_kernel(GemmProblem p) {
                 constexpr int i = decltype(ic)::value;
                 af[i][0] = *reinterpret_cast<const v4i*>(sm.a[p.st] + a0 + i * 2048);
                 af[i][1] = *reinterpret_cast<const v4i*>(sm.a[p.st] + a1 + i * 2048);
-                asc[i][0] = sm.as[0][p.s + a_s0 + i * 16 * SM::kSRow];
-                if constexpr (XF4) asc[i][F::kSub - 1] = sm.as[0][p.s + a_s1 + i * 16 * SM::kSRow];
+                asc[i] = scales(sm.as[0] + p.s + a_s + i * 16 * SM::kSRow);
             };
             auto read_b = [&](auto jc, const Place& p) {
                 constexpr int j = decltype(jc)::value;
                 bf[j][0] = *reinterpret_cast<const v4i*>(sm.b[p.st] + b0 + j * 16 * F::kWBytes);
-                bsc[j][0] = sm.bs[0][p.s + b_s0 + j * 16 * SM::kSRow];
-                if constexpr (XF4) {
-                    bf[j][1] = *reinterpret_cast<const v4i*>(sm.b[p.st] + b1 + j * 2048);
-                    bsc[j][F::kSub - 1] = sm.bs[0][p.s + b_s1 + j * 16 * SM::kSRow];
-                }
+                bsc[j] = scales(sm.bs[0] + p.s + b_s + j * 16 * SM::kSRow);
+                if constexpr (XF4) bf[j][1] = *reinterpret_cast<const v4i*>(sm.b[p.st] + b1 + j * 2048);
             };
             // (WIN, HALF) the scale bytes read for chunks past K are some other
             // row's: zero them before the last step's MFMAs
             auto cut_scales = [&](int keep) {          // 0 or ~0
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int h = 0; h < F::kSub; ++h) {
-                        asc[i][h] &= keep;
-                        bsc[i][h] &= keep;
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    asc[i] &= keep;
+                    bsc[i] &= keep;
+                }
             };
             v4f acc[8][8];
             auto wide = [](const v4i& x) { return v8i{x.x, x.y, x.z, x.w, 0, 0, 0, 0}; };
@@ -339,8 +339,7 @@ linear4_tile_kernel(GemmProblem p) {
                         constexpr int r = i + decltype(dc)::value;
                         const v4f c = decltype(firstc)::value && h == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : acc[r][j];
                         acc[r][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            wide(bf[j][h * (F::kSub - 1)]), wide(af[r][h]), c, 4, 4, 0, bsc[j][h * (F::kSub - 1)], 0,
-                            asc[r][h * (F::kSub - 1)]);
+                            wide(bf[j][h * (F::kSub - 1)]), wide(af[r][h]), c, 4, 4, h, bsc[j], h, asc[r]);
                     });
                 } else {
                     constexpr int i = i0 + t % 4;
@@ -348,7 +347,7 @@ linear4_tile_kernel(GemmProblem p) {
                                 af[i][1].x, af[i][1].y, af[i][1].z, af[i][1].w};
                     const v4f c = decltype(firstc)::value ? v4f{0.f, 0.f, 0.f, 0.f} : acc[i][j];
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(bf[j][0]), x, c, 4, 0, 0,
-                                                                                 bsc[j][0], 0, asc[i][0]);
+                                                                                 bsc[j], 0, asc[i]);
                 }
             };
             // The accumulators take all 256 AGPRs.  Held there between the steps,
