@@ -1218,7 +1218,8 @@ mx_status moe_combine_bwd(const void* dout, int64_t T, int64_t H, int32_t k,
 // ---- the MoE layer for a few tokens ----------------------------------------------
 namespace {
 struct LayerWs {
-    size_t n_act, act, tok, r, xq, xqs, z, zs, total;
+    size_t n_act, act, tok, r, xq, xqs, z, zs, parts, total;
+    int split;
 };
 LayerWs layer_ws(int32_t wdtype, int64_t T, int32_t E, int32_t k, int64_t H, int64_t F) {
     const bool mxw = wdtype != MX_DTYPE_BF16;
@@ -1233,6 +1234,8 @@ LayerWs layer_ws(int32_t wdtype, int64_t T, int32_t E, int32_t k, int64_t H, int
     L.xqs = c.take(mxw ? (size_t)(T * H / 32) : 0);
     L.z = c.take((size_t)(rows * F) * (mxw ? 1 : 2));
     L.zs = c.take(mxw ? (size_t)(rows * F / 32) : 0);
+    L.split = mx::layer_split(!mxw, T, H);
+    L.parts = c.take(L.split > 1 ? (size_t)(L.split * T * H) * 4 : 0);
     L.total = c.off;
     return L;
 }
@@ -1299,6 +1302,8 @@ mx_status moe_layer_fwd(int32_t wdtype, const void* x, const float* d_logits, in
     p.xqs = b + L.xqs;
     p.z = b + L.z;
     p.zs = b + L.zs;
+    p.split = L.split;
+    p.parts = reinterpret_cast<float*>(b + L.parts);
     const mx::LayerWeights wf = wdtype == MX_DTYPE_BF16 ? mx::LayerWeights::kBf16
                               : wdtype == MX_DTYPE_MXFP8 ? mx::LayerWeights::kMxfp8
                                                          : mx::LayerWeights::kMxfp4;

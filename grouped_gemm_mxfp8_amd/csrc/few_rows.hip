@@ -25,9 +25,14 @@ namespace {
 
 using namespace few;
 
+__device__ __forceinline__ int64_t uni64(int64_t v) {
+    const uint32_t lo = (uint32_t)uni((int)(uint32_t)v), hi = (uint32_t)uni((int)(uint32_t)((uint64_t)v >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // ---- GroupedLinear, few rows an expert --------------------------------------
 
-constexpr int kLinRows = 64;      // rows of W (columns of y) per workgroup
+constexpr int kLinRows = 64;      // rows of W (columns of y) per unit
 constexpr int kLinWaves = 4;
 
 struct LinearArgs {
@@ -36,73 +41,115 @@ struct LinearArgs {
     const float* rscale;
     uint16_t* y;
     int64_t N, K;
+    int G;
 };
 
-// One chunk of up to 16 NT rows [m0, m0 + rows) of expert e: y[.., n0 .. n0+63].
-template <int XF, int NT, bool ODD>
-__device__ __forceinline__ void linear_chunk(const LinearArgs& p, int e, int64_t n0, int64_t m0, int rows,
-                                             float* part, int wave, int lane) {
-    const int q = lane >> 4, r16 = lane & 15;
-    Row w[4], x[NT];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        // tiles past N (N % 32 == 0) repeat the first one and are not stored
-        const int64_t n = n0 + 16 * t < p.N ? n0 + 16 * t : n0;
-        w[t] = row_of<kFp4>(p.w, p.ws, (int64_t)e * p.N + n + r16, p.K, lane);
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-        x[n] = row_of<XF>(p.x, p.xs, m0 + min(n * 16 + r16, rows - 1), p.K, lane);
-    v4f acc[4][NT];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[t][n] = v4f{0.f, 0.f, 0.f, 0.f};
-    const int steps = (int)((p.K + 127) / 128);
-    const int s0 = uni(wave * steps / kLinWaves), s1 = uni((wave + 1) * steps / kLinWaves);
-    mac_rows<kFp4, XF, 4, NT, 4, ODD>(acc, w, x, s0, s1, p.K, q);
-    // the waves' K parts, added in wave order; thread (token, 4 columns)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        if (n * 16 >= rows) break;
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            *reinterpret_cast<v4f*>(part + ((wave * 4 + t) * 64 + lane) * 4) = acc[t][n];
-        __syncthreads();
-        const int tid = wave * 64 + lane;
-        const int tok = tid >> 4, c4 = tid & 15;          // columns n0 + 4 c4 .. + 3
-        const int at = ((c4 >> 2) * 64 + (c4 & 3) * 16 + tok) * 4;
-        v4f s = *reinterpret_cast<const v4f*>(part + at);
-#pragma unroll
-        for (int v = 1; v < kLinWaves; ++v) s += *reinterpret_cast<const v4f*>(part + v * 1024 + at);
-        const int row = n * 16 + tok;
-        const int64_t col = n0 + 4 * c4;
-        if (row < rows && col < p.N) {
-            const float f = p.rscale ? p.rscale[m0 + row] : 1.0f;
-            *reinterpret_cast<uint2*>(p.y + (m0 + row) * p.N + col) =
-                make_uint2(bf16x2(s[0] * f, s[1] * f), bf16x2(s[2] * f, s[3] * f));
-        }
-    }
-}
-
-template <int XF, int NTMAX, bool ODD>
-__global__ void __launch_bounds__(256)
+// A workgroup's units: 64 columns of y for up to 16 NT rows of one expert, the
+// four waves a quarter of K each.  Units run over (expert with rows, column
+// block), and over an expert's row chunks within one.
+template <int XF, int NT, int kSteps, bool ODD>
+__global__ void __launch_bounds__(64 * kLinWaves, 2)
 linear4_few_kernel(LinearArgs p) {
-    __shared__ __attribute__((aligned(16))) float part[kLinWaves * 1024];
-    const int e = blockIdx.y;
-    const int64_t lo = p.offs[e], hi = p.offs[e + 1];
-    const int wave = uni(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t n0 = (int64_t)blockIdx.x * kLinRows;
-    for (int64_t m0 = lo; m0 < hi; m0 += 16 * NTMAX) {
-        const int rows = uni((int)min((int64_t)(16 * NTMAX), hi - m0));
-        if (NTMAX > 1 && rows > 16) {
-            if (NTMAX > 2 && rows > 32) linear_chunk<XF, NTMAX, ODD>(p, e, n0, m0, rows, part, wave, lane);
-            else linear_chunk<XF, NTMAX < 2 ? NTMAX : 2, ODD>(p, e, n0, m0, rows, part, wave, lane);
-        } else {
-            linear_chunk<XF, 1, ODD>(p, e, n0, m0, rows, part, wave, lane);
+    __shared__ __attribute__((aligned(16))) float parts[2][kLinWaves * 1024];
+    __shared__ int s_count;
+    __shared__ int64_t s_lo[kMaxGroups], s_hi[kMaxGroups];    // experts with rows, in order
+    __shared__ int s_e[kMaxGroups];
+    const int tid = threadIdx.x, wave = uni(tid >> 6), lane = tid & 63;
+    if (wave == 0) {
+        int n = 0;
+        for (int e0 = 0; e0 < p.G; e0 += 64) {
+            const int e = e0 + lane;
+            int64_t lo = 0, hi = 0;
+            if (e < p.G) {
+                lo = p.offs[e];
+                hi = p.offs[e + 1];
+            }
+            const uint64_t has = __ballot(hi > lo);
+            if (hi > lo) {
+                const int at = n + __popcll(has & ((1ull << lane) - 1));
+                s_e[at] = e;
+                s_lo[at] = lo;
+                s_hi[at] = hi;
+            }
+            n += __popcll(has);
         }
+        if (lane == 0) s_count = n;
     }
+    __syncthreads();
+    const int ncol = (int)((p.N + kLinRows - 1) / kLinRows);
+    const int64_t units = (int64_t)uni(s_count) * ncol;
+    const int steps = (int)((p.K + 127) / 128);
+    // waves past the number of steps repeat step 0; their sums are not added
+    const int waves = min(kLinWaves, steps);
+    const int s0 = wave < waves ? wave * steps / waves : 0;
+    const int s1 = wave < waves ? (wave + 1) * steps / waves : 1;
+    using U = Unit<4>;
+    auto place = [&](U& u, int id, int64_t m0) -> bool {      // rows from m0, or the expert's first (m0 < 0)
+        if (id >= units) return false;
+        const int i = id / ncol;
+        const int64_t n0 = (int64_t)(id - i * ncol) * kLinRows;
+        const int64_t e = uni(s_e[i]);
+        const int64_t lo = uni64(s_lo[i]), hi = uni64(s_hi[i]);
+        u.row0 = m0 < 0 ? lo : m0;
+        u.rows = (int)min((int64_t)(16 * NT), hi - u.row0);
+        u.s0 = s0;
+        u.s1 = s1;
+        u.id = id;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            // tiles past N (N % 32 == 0) repeat the first one and are not stored
+            const int64_t r = e * p.N + (n0 + 16 * t < p.N ? n0 + 16 * t : n0);
+            u.wc[t] = p.w + r * (p.K / 2);
+            u.ws[t] = p.ws + r * (p.K / 32);
+        }
+        return true;
+    };
+    int turn = 0;
+    float scale[NT];                 // row scale of this thread's token in done
+    stream<kFp4, XF, 4, NT, kSteps, ODD>(
+        p.K, lane, [&](U& u) { return place(u, blockIdx.x, -1); },
+        [&](U& u) {
+            const int64_t hi = uni64(s_hi[u.id / ncol]);
+            if (u.row0 + 16 * NT < hi) return place(u, u.id, u.row0 + 16 * NT);
+            return place(u, u.id + (int)gridDim.x, -1);
+        },
+        [&](const U& u, int n) {
+            return x_row<XF>(p.x, p.xs, u.row0 + min(n * 16 + (lane & 15), u.rows - 1), p.K, lane);
+        },
+        [&](const U& u) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                scale[n] = p.rscale ? p.rscale[u.row0 + min(n * 16 + (tid >> 4), u.rows - 1)] : 1.0f;
+        },
+        [&](const v4f(&acc)[4][NT], const U& u) {
+            const int64_t n0 = (int64_t)(u.id % ncol) * kLinRows;
+            // the waves' K parts, added in wave order; thread (token, 4 columns).  Two
+            // buffers in turn: a wave that writes one has passed the barrier of the
+            // other, and with it everybody's reads of this one.
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (n * 16 >= u.rows) break;
+                float* const part = parts[turn];
+                turn ^= 1;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    *reinterpret_cast<v4f*>(part + ((wave * 4 + t) * 64 + lane) * 4) = acc[t][n];
+                __syncthreads();
+                const int tok = tid >> 4, c4 = tid & 15;          // columns n0 + 4 c4 .. + 3
+                const int at = ((c4 >> 2) * 64 + (c4 & 3) * 16 + tok) * 4;
+                v4f s = *reinterpret_cast<const v4f*>(part + at);
+#pragma unroll
+                for (int v = 1; v < kLinWaves; ++v)
+                    if (v < waves) s += *reinterpret_cast<const v4f*>(part + v * 1024 + at);
+                const int row = n * 16 + tok;
+                const int64_t col = n0 + 4 * c4;
+                if (row < u.rows && col < p.N) {
+                    const float f = scale[n];
+                    *reinterpret_cast<uint2*>(p.y + (u.row0 + row) * p.N + col) =
+                        make_uint2(bf16x2(s[0] * f, s[1] * f), bf16x2(s[2] * f, s[3] * f));
+                }
+            }
+        });
 }
 
 // ---- the layer: plan ---------------------------------------------------------
@@ -275,193 +322,291 @@ layer_prep_kernel(LayerArgs p) {
 
 constexpr int kGuWaves = 4;
 
-// Rows [c0, c0 + rows) of the expert's list, columns f0 .. f0 + 31 of z.
-template <int WF, int NT>
-__device__ __forceinline__ void gate_up_chunk(const LayerArgs& p, int e, int row0, int rows, int64_t f0,
-                                              float* part, int wave, int lane) {
-    constexpr int XF = WF == kBf16 ? kBf16 : kFp8;
-    const int q = lane >> 4, r16 = lane & 15;
-    Row w[4], x[NT];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)      // tiles 0, 1: gate rows; 2, 3: up rows
-        w[t] = row_of<WF>(p.w1, p.w1s, (int64_t)e * 2 * p.F + (t >> 1) * p.F + f0 + (t & 1) * 16 + r16, p.H,
-                          lane);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int tok = p.plan.tok[row0 + min(n * 16 + r16, rows - 1)];
-        x[n] = row_of<XF>(WF == kBf16 ? reinterpret_cast<const uint8_t*>(p.x) : p.xq, p.xqs, tok, p.H, lane);
+// LDS copy of the plan: the routed experts and the rows' tokens.
+struct PlanLds {
+    int4* act;
+    int* tok;
+    float* r;
+    int n_act;
+};
+size_t plan_lds_bytes(const LayerArgs& p) {
+    const int64_t rows = p.T * p.k, experts = p.E < rows ? p.E : rows;
+    return (size_t)(experts * 16 + rows * 8);
+}
+__device__ __forceinline__ PlanLds read_plan(const LayerArgs& p, uint8_t* smem) {
+    const int rows = (int)p.T * p.k, experts = min(p.E, rows);
+    PlanLds l{reinterpret_cast<int4*>(smem), reinterpret_cast<int*>(smem + experts * 16),
+              reinterpret_cast<float*>(smem + experts * 16 + rows * 4), 0};
+    // (entries past the routed ones are not initialised and not used)
+    for (int i = threadIdx.x; i < experts; i += blockDim.x) l.act[i] = p.plan.act[i];
+    for (int i = threadIdx.x; i < rows; i += blockDim.x) {
+        l.tok[i] = p.plan.tok[i];
+        l.r[i] = p.plan.r[i];
     }
-    v4f acc[4][NT];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[t][n] = v4f{0.f, 0.f, 0.f, 0.f};
-    const int steps = (int)(p.H / 128);
-    const int s0 = uni(wave * steps / kGuWaves), s1 = uni((wave + 1) * steps / kGuWaves);
-    mac_rows<WF, XF, 4, NT, 4 / loads_per_step(WF), false>(acc, w, x, s0, s1, p.H, q);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        if (n * 16 >= rows) break;
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            *reinterpret_cast<v4f*>(part + ((wave * 4 + t) * 64 + lane) * 4) = acc[t][n];
-        __syncthreads();
-        // thread (token, two columns f0 + 2 c, + 1): the 16 threads of a token
-        // are one DPP row and hold one block of 32
-        const int tid = wave * 64 + lane;
-        const int tok = tid >> 4, c = (tid & 15) * 2;
-        const int at = ((c >> 4) * 64 + ((c & 15) >> 2) * 16 + tok) * 4 + (c & 3);
-        float g[2] = {0.f, 0.f}, u[2] = {0.f, 0.f};
-#pragma unroll
-        for (int v = 0; v < kGuWaves; ++v) {
-            const float2 a = *reinterpret_cast<const float2*>(part + v * 1024 + at);
-            const float2 b = *reinterpret_cast<const float2*>(part + v * 1024 + 512 + at);
-            g[0] += a.x;
-            g[1] += a.y;
-            u[0] += b.x;
-            u[1] += b.y;
-        }
-        const int row = n * 16 + tok;
-        const bool live = row < rows;
-        const float r = live ? p.plan.r[row0 + row] : 0.f;
-        float z[2];
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-            z[v] = r * (g[v] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[v])) * u[v]);
-        const int64_t zrow = row0 + row;
-        if constexpr (WF == kBf16) {
-            if (live)
-                *reinterpret_cast<uint32_t*>(p.z + (zrow * p.F + f0 + c) * 2) = bf16x2(z[0], z[1]);
-        } else {
-            uint32_t m = max(abs_bits(z[0]), abs_bits(z[1]));
-            m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, false));
-            m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, false));
-            m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x124, 0xF, 0xF, false));
-            m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x128, 0xF, 0xF, false));
-            const bool bad = m >= 0x7f800000u;
-            const uint32_t sc = bad ? 255u : scale_code_from_amax_bits(m);
-            const uint32_t o = bad ? 0u : e4m3x2_scaled(0u, z[0], z[1], e4m3_limit_from_code(sc),
-                                                        scale_from_code(sc), false);
-            if (live) {
-                *reinterpret_cast<uint16_t*>(p.z + zrow * p.F + f0 + c) = (uint16_t)o;
-                if (c == 0) p.zs[zrow * (p.F / 32) + f0 / 32] = (uint8_t)sc;
-            }
-        }
-    }
+    l.n_act = uni(*p.plan.n_act);
+    __syncthreads();
+    return l;
 }
 
-template <int WF, int NTMAX>
-__global__ void __launch_bounds__(256)
+// A workgroup's units: 32 columns of z (tiles 0, 1: their gate rows of W1; 2, 3:
+// the up rows) for up to 16 NT rows of one routed expert, the four waves a
+// quarter of H each.
+template <int WF, int NT, int kSteps>
+__global__ void __launch_bounds__(64 * kGuWaves, 2)
 layer_gate_up_kernel(LayerArgs p) {
-    __shared__ __attribute__((aligned(16))) float part[kGuWaves * 1024];
-    if ((int)blockIdx.y >= *p.plan.n_act) return;
-    const int4 a = p.plan.act[blockIdx.y];
-    const int e = uni(a.x), first = uni(a.y), count = uni(a.z);
-    const int wave = uni(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t f0 = (int64_t)blockIdx.x * 32;
-    for (int c0 = 0; c0 < count; c0 += 16 * NTMAX) {
-        const int rows = min(16 * NTMAX, count - c0);
-        if (NTMAX > 1 && rows > 16) {
-            if (NTMAX > 2 && rows > 32) gate_up_chunk<WF, NTMAX>(p, e, first + c0, rows, f0, part, wave, lane);
-            else gate_up_chunk<WF, NTMAX < 2 ? NTMAX : 2>(p, e, first + c0, rows, f0, part, wave, lane);
-        } else {
-            gate_up_chunk<WF, 1>(p, e, first + c0, rows, f0, part, wave, lane);
+    constexpr int XF = WF == kBf16 ? kBf16 : kFp8;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    __shared__ __attribute__((aligned(16))) float parts[2][kGuWaves * 1024];
+    const int tid = threadIdx.x, wave = uni(tid >> 6), lane = tid & 63;
+    const PlanLds plan = read_plan(p, smem);
+    const int ncol = (int)(p.F / 32), units = plan.n_act * ncol;
+    const int steps = (int)(p.H / 128);
+    // waves past the number of steps repeat step 0; their sums are not added
+    const int waves = min(kGuWaves, steps);
+    const int s0 = wave < waves ? wave * steps / waves : 0;
+    const int s1 = wave < waves ? (wave + 1) * steps / waves : 1;
+    const int64_t wb = row_bytes(WF, p.H), sb = p.H / 32;
+    using U = Unit<4>;
+    auto place = [&](U& u, int id, int c0) -> bool {       // the expert's rows from its c0-th
+        if (id >= units) return false;
+        const int a = id / ncol;
+        const int4 ex = plan.act[a];
+        const int64_t e = uni(ex.x);
+        u.row0 = uni(ex.y) + c0;
+        u.rows = min(16 * NT, uni(ex.z) - c0);
+        u.s0 = s0;
+        u.s1 = s1;
+        u.id = id;
+        const int64_t f0 = (int64_t)(id - a * ncol) * 32;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int64_t r = e * 2 * p.F + (t >> 1) * p.F + f0 + (t & 1) * 16;
+            u.wc[t] = p.w1 + r * wb;
+            u.ws[t] = WF == kBf16 ? nullptr : p.w1s + r * sb;
         }
-    }
+        return true;
+    };
+    int turn = 0;
+    stream<WF, XF, 4, NT, kSteps, false>(
+        p.H, lane, [&](U& u) { return place(u, blockIdx.x, 0); },
+        [&](U& u) {
+            const int4 ex = plan.act[u.id / ncol];
+            const int c0 = (int)u.row0 - uni(ex.y) + 16 * NT;
+            if (c0 < uni(ex.z)) return place(u, u.id, c0);
+            return place(u, u.id + (int)gridDim.x, 0);
+        },
+        [&](const U& u, int n) {
+            const int tok = plan.tok[(int)u.row0 + min(n * 16 + (lane & 15), u.rows - 1)];
+            return x_row<XF>(WF == kBf16 ? reinterpret_cast<const uint8_t*>(p.x) : p.xq, p.xqs, tok, p.H, lane);
+        },
+        [](const U&) {},
+        [&](const v4f(&acc)[4][NT], const U& u) {
+            const int64_t f0 = (int64_t)(u.id % ncol) * 32;
+            // (buffers in turn as in linear4_few_kernel)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (n * 16 >= u.rows) break;
+                float* const part = parts[turn];
+                turn ^= 1;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    *reinterpret_cast<v4f*>(part + ((wave * 4 + t) * 64 + lane) * 4) = acc[t][n];
+                // thread (token, two columns f0 + 2 c, + 1): the 16 threads of a token
+                // are one DPP row and hold one block of 32
+                const int tok = tid >> 4, c = (tid & 15) * 2;
+                const int row = n * 16 + tok;
+                const bool live = row < u.rows;
+                const int64_t zrow = u.row0 + row;
+                const float r = live ? plan.r[zrow] : 0.f;
+                __syncthreads();
+                const int at = ((c >> 4) * 64 + ((c & 15) >> 2) * 16 + tok) * 4 + (c & 3);
+                float g[2] = {0.f, 0.f}, up[2] = {0.f, 0.f};
+#pragma unroll
+                for (int v = 0; v < kGuWaves; ++v)
+                    if (v < waves) {
+                        const float2 a = *reinterpret_cast<const float2*>(part + v * 1024 + at);
+                        const float2 b = *reinterpret_cast<const float2*>(part + v * 1024 + 512 + at);
+                        g[0] += a.x;
+                        g[1] += a.y;
+                        up[0] += b.x;
+                        up[1] += b.y;
+                    }
+                float z[2];
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+                    z[v] = r * (g[v] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[v])) * up[v]);
+                if constexpr (WF == kBf16) {
+                    if (live)
+                        *reinterpret_cast<uint32_t*>(p.z + (zrow * p.F + f0 + c) * 2) = bf16x2(z[0], z[1]);
+                } else {
+                    uint32_t m = max(abs_bits(z[0]), abs_bits(z[1]));
+                    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, false));
+                    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, false));
+                    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x124, 0xF, 0xF, false));
+                    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x128, 0xF, 0xF, false));
+                    const bool bad = m >= 0x7f800000u;
+                    const uint32_t sc = bad ? 255u : scale_code_from_amax_bits(m);
+                    const uint32_t o = bad ? 0u : e4m3x2_scaled(0u, z[0], z[1], e4m3_limit_from_code(sc),
+                                                                scale_from_code(sc), false);
+                    if (live) {
+                        *reinterpret_cast<uint16_t*>(p.z + zrow * p.F + f0 + c) = (uint16_t)o;
+                        if (c == 0) p.zs[zrow * (p.F / 32) + f0 / 32] = (uint8_t)sc;
+                    }
+                }
+            }
+        });
 }
 
 // ---- the layer: down and combine -------------------------------------------------
 
 constexpr int kDnWaves = 8;
+constexpr int kSplitFull = 256;    // workgroups of the down projection, one a CU
 
-// z rows [row0, row0 + rows) against rows h0 .. h0 + 15 of expert e's W2 over
-// the steps [s0, s1): added to the wave's sums out[token][16].
-template <int WF, int NT>
-__device__ __forceinline__ void down_unit(const LayerArgs& p, int e, int row0, int rows, int64_t h0, int s0,
-                                          int s1, float* out, int lane) {
-    constexpr int XF = WF == kBf16 ? kBf16 : kFp8;
-    const int q = lane >> 4, r16 = lane & 15;
-    Row w[1], x[NT];
-    w[0] = row_of<WF>(p.w2, p.w2s, (int64_t)e * p.H + h0 + r16, p.F, lane);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-        x[n] = row_of<XF>(p.z, p.zs, row0 + min(n * 16 + r16, rows - 1), p.F, lane);
-    v4f acc[1][NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[0][n] = v4f{0.f, 0.f, 0.f, 0.f};
-    mac_rows<WF, XF, 1, NT, 8 / loads_per_step(WF), false>(acc, w, x, s0, s1, p.F, q);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int row = n * 16 + r16;
-        if (row < rows) {       // an expert's tokens are distinct: no two lanes share a sum
-            v4f* o = reinterpret_cast<v4f*>(out + p.plan.tok[row0 + row] * 16 + 4 * q);
-            *o += acc[0][n];
-        }
-    }
+// 16-row tiles of W2 a workgroup takes; z is read once for all of them, and for
+// MX weights one tile of z rows is as many bytes (MXFP4: twice) as one tile of
+// W2.  One tile: H / 16 workgroups fill the CUs and no sums of parts are left to
+// add.  Measured on 8 x (4096, 14336) MXFP4, all experts, one / two / four tiles:
+// T = 4 60 / - / - us, T = 16 92 / 68 / 67, T = 32 - / 94 / 78; 64 tokens on 64 x
+// (2048, 1408) 35 / 28 / - (four tiles of 128 tokens' sums do not fit the LDS);
+// bf16, 16 tokens: 155 / 156 / 170.
+constexpr int down_tiles(bool bf16, int64_t T) {
+    return T <= 4 || (bf16 && T <= 16) ? 1 : T <= 16 || T > 32 || bf16 ? 2 : 4;
 }
 
-// TMAX: bound of T that sizes the sums in LDS.
-template <int WF, int NTMAX, int TMAX>
-__global__ void __launch_bounds__(64 * kDnWaves)
+// `split` workgroups share rows h0 .. h0 + 16 RT - 1 of every routed expert's W2.  Their
+// waves' units are (expert, part of F, chunk of rows); each wave adds its units'
+// products to its own sums[token][16], and the waves' sums are added in order.
+// With split > 1 a workgroup leaves its sums in `parts` and layer_sum adds them.
+// (Adding them in the last workgroup to arrive took six times as long: the
+// fences that such a hand-over needs write the XCD's L2 back, 0.3 us each.)
+// TMAX: bound of T that sizes the sums.
+template <int WF, int NT, int kSteps, int RT, int TMAX>
+__global__ void __launch_bounds__(64 * kDnWaves, 2)
 layer_down_kernel(LayerArgs p) {
-    __shared__ __attribute__((aligned(16))) float sums[kDnWaves * TMAX * 16];
+    constexpr int XF = WF == kBf16 ? kBf16 : kFp8;
+    constexpr int kCols = 16 * RT;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    __shared__ __attribute__((aligned(16))) float sums[kDnWaves * TMAX * 16 * RT];
     const int tid = threadIdx.x, wave = uni(tid >> 6), lane = tid & 63;
-    const int64_t h0 = (int64_t)blockIdx.x * 16;
+    const int64_t h0 = (int64_t)(blockIdx.x / p.split) * kCols;
+    const int part = blockIdx.x % p.split, waves = kDnWaves * p.split;
     const int T = (int)p.T;
-    float* out = sums + wave * TMAX * 16;
-    for (int i = lane; i < T * 4; i += 64) reinterpret_cast<v4f*>(out)[i] = v4f{0.f, 0.f, 0.f, 0.f};
-    const int n_act = uni(*p.plan.n_act);
+    float* out = sums + wave * TMAX * kCols;
+    for (int i = lane; i < T * 4 * RT; i += 64) reinterpret_cast<v4f*>(out)[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    const PlanLds plan = read_plan(p, smem);
     const int steps = (int)(p.F / 128);
-    // K parts per expert, so that every wave has work with few experts
-    const int parts = uni(max(1, min(steps / 4, (2 * kDnWaves + n_act - 1) / max(n_act, 1))));
-    for (int u = wave; u < n_act * parts; u += kDnWaves) {
-        const int a = u / parts, c = u - a * parts;
-        const int4 ex = p.plan.act[a];
-        const int e = uni(ex.x), first = uni(ex.y), count = uni(ex.z);
-        const int s0 = uni(c * steps / parts), s1 = uni((c + 1) * steps / parts);
-        for (int c0 = 0; c0 < count; c0 += 16 * NTMAX) {
-            const int rows = min(16 * NTMAX, count - c0);
-            if (NTMAX > 1 && rows > 16) {
-                if (NTMAX > 2 && rows > 32) down_unit<WF, NTMAX>(p, e, first + c0, rows, h0, s0, s1, out, lane);
-                else down_unit<WF, NTMAX < 2 ? NTMAX : 2>(p, e, first + c0, rows, h0, s0, s1, out, lane);
-            } else {
-                down_unit<WF, 1>(p, e, first + c0, rows, h0, s0, s1, out, lane);
-            }
+    // parts of F per expert, so that every wave has work with few experts
+    const int parts = max(1, min((steps + kSteps - 1) / kSteps,
+                                 (2 * waves + plan.n_act - 1) / max(plan.n_act, 1)));
+    const int units = plan.n_act * parts;
+    const int64_t wb = row_bytes(WF, p.F), sb = p.F / 32;
+    using U = Unit<RT>;
+    auto place = [&](U& u, int id, int c0) -> bool {
+        if (id >= units) return false;
+        const int a = id / parts, c = id - a * parts;
+        const int4 ex = plan.act[a];
+        u.row0 = uni(ex.y) + c0;
+        u.rows = min(16 * NT, uni(ex.z) - c0);
+        u.s0 = c * steps / parts;
+        u.s1 = (c + 1) * steps / parts;
+        u.id = id;
+        const int64_t r = (int64_t)uni(ex.x) * p.H + h0;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            u.wc[t] = p.w2 + (r + 16 * t) * wb;
+            u.ws[t] = WF == kBf16 ? nullptr : p.w2s + (r + 16 * t) * sb;
         }
-    }
+        return true;
+    };
+    stream<WF, XF, RT, NT, kSteps, false>(
+        p.F, lane, [&](U& u) { return place(u, part * kDnWaves + wave, 0); },
+        [&](U& u) {
+            const int4 ex = plan.act[u.id / parts];
+            const int c0 = (int)u.row0 - uni(ex.y) + 16 * NT;
+            if (c0 < uni(ex.z)) return place(u, u.id, c0);
+            return place(u, u.id + waves, 0);
+        },
+        [&](const U& u, int n) {
+            return x_row<XF>(p.z, p.zs, u.row0 + min(n * 16 + (lane & 15), u.rows - 1), p.F, lane);
+        },
+        [](const U&) {},
+        [&](const v4f(&acc)[RT][NT], const U& u) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int row = n * 16 + (lane & 15);
+                if (row < u.rows) {       // an expert's tokens are distinct: no two lanes share a sum
+                    float* o = out + plan.tok[(int)u.row0 + row] * kCols + 4 * (lane >> 4);
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) *reinterpret_cast<v4f*>(o + 16 * t) += acc[t][n];
+                }
+            }
+        });
     __syncthreads();
-    for (int i = tid; i < T * 8; i += 64 * kDnWaves) {        // two rows of out a thread
+    for (int i = tid; i < T * 8 * RT; i += 64 * kDnWaves) {        // two columns of a token a thread
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < kDnWaves; ++v) {
-            const float2 a = *reinterpret_cast<const float2*>(sums + v * TMAX * 16 + 2 * i);
+            const float2 a = *reinterpret_cast<const float2*>(sums + v * TMAX * kCols + 2 * i);
             s.x += a.x;
             s.y += a.y;
         }
-        *reinterpret_cast<uint32_t*>(p.out + (int64_t)(i >> 3) * p.H + h0 + 2 * (i & 7)) = bf16x2(s.x, s.y);
+        const int64_t at = (int64_t)(i / (8 * RT)) * p.H + h0 + 2 * (i % (8 * RT));
+        if (p.split == 1) *reinterpret_cast<uint32_t*>(p.out + at) = bf16x2(s.x, s.y);
+        else *reinterpret_cast<float2*>(p.parts + (int64_t)part * T * p.H + at) = s;
     }
+}
+
+// out = the sums of the split workgroups, in their order; eight columns a thread.
+__global__ void __launch_bounds__(256)
+layer_sum_kernel(LayerArgs p) {
+    const int64_t n = p.T * p.H, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= n) return;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int v = 0; v < p.split; ++v) {
+        const v4f* a = reinterpret_cast<const v4f*>(p.parts + (int64_t)v * n + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += a[j >> 2][j & 3];
+    }
+    *reinterpret_cast<uint4*>(p.out + i) =
+        make_uint4(bf16x2(s[0], s[1]), bf16x2(s[2], s[3]), bf16x2(s[4], s[5]), bf16x2(s[6], s[7]));
+}
+
+template <int WF, int NT, int TMAX>
+hipError_t launch_layer_rows(const LayerArgs& p, hipStream_t s) {
+    // 16 (NT > 1: 8) loads of 16 bytes a lane and group in gate-up, 4 a tile in down
+    constexpr int L = loads_per_step(WF);
+    constexpr int gs = NT == 1 || L == 4 ? 4 / L : 2 / L < 1 ? 1 : 2 / L, rt = down_tiles(WF == kBf16, TMAX),
+                  ds = rt * NT >= 8 && L < 4 ? 2 / L : 4 / L;
+    const int64_t rows = p.T * p.k, experts = p.E < rows ? p.E : rows;
+    const size_t lds = plan_lds_bytes(p);
+    const int64_t units = experts * (p.F / 32);
+    const int64_t fit = 2 * device_cu_count();
+    hipLaunchKernelGGL((layer_gate_up_kernel<WF, NT, gs>), dim3((unsigned)(units < fit ? units : fit)),
+                       dim3(64 * kGuWaves), lds, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((layer_down_kernel<WF, NT, ds, rt, TMAX>), dim3((unsigned)(p.H / (16 * rt) * p.split)),
+                       dim3(64 * kDnWaves), lds, s, p);
+    if (p.split > 1)
+        hipLaunchKernelGGL(layer_sum_kernel, dim3((unsigned)((p.T * p.H / 8 + 255) / 256)), dim3(256), 0, s, p);
+    return hipGetLastError();
 }
 
 template <int WF>
 hipError_t launch_layer_fmt(const LayerArgs& p, hipStream_t s) {
-    const dim3 gu((unsigned)(p.F / 32), (unsigned)(p.E < p.T * p.k ? p.E : p.T * p.k));
-    const dim3 dn((unsigned)(p.H / 16));
-    if (p.T <= 16) hipLaunchKernelGGL((layer_gate_up_kernel<WF, 1>), gu, dim3(256), 0, s, p);
-    else if (p.T <= 32) hipLaunchKernelGGL((layer_gate_up_kernel<WF, 2>), gu, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((layer_gate_up_kernel<WF, 4>), gu, dim3(256), 0, s, p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (p.T <= 16) hipLaunchKernelGGL((layer_down_kernel<WF, 1, 16>), dn, dim3(64 * kDnWaves), 0, s, p);
-    else if (p.T <= 32) hipLaunchKernelGGL((layer_down_kernel<WF, 2, 32>), dn, dim3(64 * kDnWaves), 0, s, p);
-    else hipLaunchKernelGGL((layer_down_kernel<WF, 4, kLayerMaxTokens>), dn, dim3(64 * kDnWaves), 0, s, p);
-    return hipGetLastError();
+    if (p.T <= 4) return launch_layer_rows<WF, 1, 4>(p, s);
+    if (p.T <= 16) return launch_layer_rows<WF, 1, 16>(p, s);
+    if (p.T <= 32) return launch_layer_rows<WF, 2, 32>(p, s);
+    return launch_layer_rows<WF, 4, kLayerMaxTokens>(p, s);
 }
 
 template <int XF, bool ODD>
-void launch_few(const LinearArgs& a, dim3 grid, int64_t M, hipStream_t s) {
-    if (M <= 16) hipLaunchKernelGGL((linear4_few_kernel<XF, 1, ODD>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((linear4_few_kernel<XF, 4, ODD>), grid, dim3(256), 0, s, a);
+void launch_few(const LinearArgs& a, int64_t M, hipStream_t s) {
+    const int64_t units = (M < a.G ? M : a.G) * ((a.N + kLinRows - 1) / kLinRows);
+    const int64_t fit = 2 * device_cu_count();
+    const dim3 grid((unsigned)(units < fit ? units : fit));
+    if (M <= 16) hipLaunchKernelGGL((linear4_few_kernel<XF, 1, 4, ODD>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((linear4_few_kernel<XF, 4, 2, ODD>), grid, dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -469,17 +614,21 @@ void launch_few(const LinearArgs& a, dim3 grid, int64_t M, hipStream_t s) {
 hipError_t launch_linear4_few(bool x_fp4, const uint8_t* x, const uint8_t* xs, const int64_t* offs, int G,
                               int64_t M, const uint8_t* w, const uint8_t* ws, int64_t N, int64_t K,
                               const float* rscale, uint16_t* y, hipStream_t s) {
-    const LinearArgs a{x, xs, w, ws, offs, rscale, y, N, K};
-    const dim3 grid((unsigned)((N + kLinRows - 1) / kLinRows), (unsigned)G);
+    const LinearArgs a{x, xs, w, ws, offs, rscale, y, N, K, G};
     const bool odd = K % 128 != 0;
     if (x_fp4) {
-        if (odd) launch_few<kFp4, true>(a, grid, M, s);
-        else launch_few<kFp4, false>(a, grid, M, s);
+        if (odd) launch_few<kFp4, true>(a, M, s);
+        else launch_few<kFp4, false>(a, M, s);
     } else {
-        if (odd) launch_few<kFp8, true>(a, grid, M, s);
-        else launch_few<kFp8, false>(a, grid, M, s);
+        if (odd) launch_few<kFp8, true>(a, M, s);
+        else launch_few<kFp8, false>(a, M, s);
     }
     return hipGetLastError();
+}
+
+int layer_split(bool bf16, int64_t T, int64_t H) {
+    const int64_t tiles = H / (16 * down_tiles(bf16, T)), s = (kSplitFull + tiles - 1) / tiles;
+    return (int)(s < 8 ? s : 8);
 }
 
 hipError_t launch_layer(LayerWeights wf, const LayerArgs& p, hipStream_t s) {

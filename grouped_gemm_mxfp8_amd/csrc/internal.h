@@ -214,7 +214,10 @@ struct LayerArgs {
     LayerPlan plan;
     uint8_t *xq, *xqs;       // MX weights: MXFP8 copy of x
     uint8_t *z, *zs;         // [T k][F], MXFP8 (MX weights) or bf16
+    int split;               // workgroups that share columns of out (layer_split)
+    float* parts;            // split > 1: [split][T][H] partial sums
 };
+int layer_split(bool bf16, int64_t T, int64_t H);
 hipError_t launch_layer(LayerWeights wf, const LayerArgs& p, hipStream_t s);
 
 int device_cu_count();
