@@ -50,8 +50,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
 
-__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 // The operand registers of one 128-value step of one 16-row tile.
 template <int F>
 __device__ __forceinline__ v8i mx_frag(const u32x4* c) {
@@ -78,48 +76,38 @@ __device__ __forceinline__ v4f mac_step(v4f acc, const u32x4* w, uint32_t ws, co
     }
 }
 
-// A lane's place in a 16-row tile: byte offsets of its row's codes (at its 16
-// bytes of K = 0) and scales from the tile's first row.
-struct LaneRow {
-    uint32_t codes, scales;
-    int q;
-};
-template <int F>
-__device__ __forceinline__ LaneRow lane_row(int64_t K, int lane) {
-    return LaneRow{(uint32_t)((lane & 15) * row_bytes(F, K)) + (uint32_t)(lane >> 4) * 16u,
-                   (uint32_t)((lane & 15) * (K / 32)), lane >> 4};
-}
-
-// kSteps consecutive 128-value steps of one tile in registers, from the tile's
-// first row (codes, scales: wave-uniform for weights, a lane's own row with a
-// zero LaneRow for activations).  Steps at or past `last` (uniform) repeat step
-// last - 1 and are skipped by the caller: the loads stay in range without a
-// branch per lane.
-// ODD (K % 128 != 0; MX formats): 16-byte chunks past K read as zero codes,
-// their scales as 2^0, and scales are read byte by byte (their rows start at
-// any byte).
-template <int F, int kSteps, bool ODD>
+// kSteps consecutive 128-value steps of one 16-row tile in registers.
+// FULL: the number of steps is a multiple of kSteps, and a row's scales are read
+// four (two) steps at a time; else step by step, and steps past the last one
+// read what follows (their products are skipped).
+// ODD (K % 128 != 0; MX formats): 16-byte chunks past K count as zero codes with
+// scale 2^0, and scales are read byte by byte (their rows start at any byte).
+// Loads are never under a branch: the compiler counts them to know which ones
+// have arrived, and where two paths meet it waits for all.
+template <int F, int kSteps, bool FULL, bool ODD>
 struct Tile {
     static constexpr int kL = loads_per_step(F);
     u32x4 c[kSteps * kL];
     uint32_t s[F == kBf16 ? 1 : kSteps];     // 4 blocks' scales (ODD: this lane's alone)
 
-    __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, const LaneRow& r,
-                                         int step, int last, int64_t K) {
+    // first value of chunk l of step st for lane quarter q: 16 bytes are 32 E2M1
+    // or 16 E4M3 values
+    static __device__ __forceinline__ int64_t value(int st, int l, int q) {
+        return (int64_t)st * 128 + (F == kFp4 ? q * 32 : l * 64 + q * 16);
+    }
+
+    // codes16(byte), scale16/8/4(byte), scale1(byte): loads of the row at a byte of
+    // it, the lane's 16 q included for codes
+    template <class Src>
+    __device__ __forceinline__ void load(const Src& src, int step, int last, int64_t K, int q) {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int st = min(step + i, last - 1);
+            const int st = ODD || !FULL ? min(step + i, last - 1) : step + i;
 #pragma unroll
             for (int l = 0; l < kL; ++l) {
-                const uint8_t* p = codes + (int64_t)st * bytes_per_step(F) + l * 64 + r.codes;
-                if constexpr (ODD) {
-                    // first value of the chunk: E2M1 16 bytes are 32 values, E4M3 16
-                    const int64_t k0 = (int64_t)st * 128 + (F == kFp4 ? r.q * 32 : l * 64 + r.q * 16);
-                    c[i * kL + l] = u32x4{0, 0, 0, 0};
-                    if (k0 < K) c[i * kL + l] = *reinterpret_cast<const u32x4*>(p);
-                } else {
-                    c[i * kL + l] = *reinterpret_cast<const u32x4*>(p);
-                }
+                // ODD: a chunk past K reads the row's first one instead
+                const bool in = !ODD || value(st, l, q) < K;
+                c[i * kL + l] = src.codes16(in ? (uint32_t)(st * bytes_per_step(F)) : 0u, in ? l * 64 : 0);
             }
         }
         if constexpr (F == kBf16) {
@@ -127,39 +115,81 @@ struct Tile {
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
                 const int st = min(step + i, last - 1);
-                s[i] = 127;
-                if ((int64_t)st * 128 + r.q * 32 < K) s[i] = scales[(int64_t)st * 4 + r.q + r.scales];
+                const bool in = (int64_t)st * 128 + q * 32 < K;
+                s[i] = src.scale1(in ? (uint32_t)(st * 4 + q) : 0u);
             }
-        } else if (kSteps % 2 == 0 && step + kSteps <= last) {
-            const uint8_t* p = scales + (int64_t)step * 4 + r.scales;
-            if constexpr (kSteps % 4 == 0) {
+        } else if constexpr (FULL && kSteps % 4 == 0) {
 #pragma unroll
-                for (int i = 0; i + 3 < kSteps; i += 4) {
-                    const u32x4 v = *reinterpret_cast<const u32x4_a4*>(p + i * 4);
-                    s[i] = v.x;
-                    s[i + 1] = v.y;
-                    s[i + 2] = v.z;
-                    s[i + 3] = v.w;
-                }
-            } else {
+            for (int i = 0; i < kSteps; i += 4) {
+                const u32x4 v = src.scale16((uint32_t)(step + i) * 4);
+                s[i] = v.x;
+                s[i + 1] = v.y;
+                s[i + 2] = v.z;
+                s[i + 3] = v.w;
+            }
+        } else if constexpr (FULL && kSteps % 2 == 0) {
 #pragma unroll
-                for (int i = 0; i + 1 < kSteps; i += 2) {
-                    const auto v = *reinterpret_cast<const u32x2_a4*>(p + i * 4);
-                    s[i] = v.x;
-                    s[i + 1] = v.y;
-                }
+            for (int i = 0; i < kSteps; i += 2) {
+                const auto v = src.scale8((uint32_t)(step + i) * 4);
+                s[i] = v.x;
+                s[i + 1] = v.y;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i)
-                s[i] = *reinterpret_cast<const uint32_t*>(scales + (int64_t)min(step + i, last - 1) * 4 + r.scales);
+            for (int i = 0; i < kSteps; ++i) s[i] = src.scale4((uint32_t)min(step + i, last - 1) * 4);
         }
     }
-    // the scale operand of step i: this lane's block in the low byte
-    __device__ __forceinline__ uint32_t scale(int i, int q) const {
+    // the operand of step i, and its scale: this lane's block in the low byte
+    __device__ __forceinline__ void codes(u32x4 (&o)[kL], int i, int st, int64_t K, int q) const {
+#pragma unroll
+        for (int l = 0; l < kL; ++l) {
+            o[l] = c[i * kL + l];
+            if constexpr (ODD)
+                if (!(value(st, l, q) < K)) o[l] = u32x4{0, 0, 0, 0};
+        }
+    }
+    __device__ __forceinline__ uint32_t scale(int i, int st, int64_t K, int q) const {
         if constexpr (F == kBf16) return 0;
-        else if constexpr (ODD) return s[i];
+        else if constexpr (ODD) return (int64_t)st * 128 + q * 32 < K ? s[i] : 127u;
         else return s[i] >> (8 * q);
+    }
+};
+
+// Loads of a weight tile: buffer descriptors of its 16 rows (no bytes where there
+// is no tile to load: the loads return zeros and touch no memory), the lane's row
+// as an offset.
+struct WSrc {
+    __amdgpu_buffer_rsrc_t c, s;
+    uint32_t crow, srow;
+    template <int F>
+    static __device__ __forceinline__ WSrc of(const uint8_t* codes, const uint8_t* scales, int64_t K,
+                                              bool live, int lane) {
+        const int cb = (int)row_bytes(F, K), sb = F == kBf16 ? 0 : (int)(K / 32);
+        return WSrc{__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(codes), 0, live ? 16 * cb : 0, 0x20000),
+                    __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(scales), 0, live ? 16 * sb : 0, 0x20000),
+                    (uint32_t)((lane & 15) * cb + (lane >> 4) * 16), (uint32_t)((lane & 15) * sb)};
+    }
+    __device__ __forceinline__ u32x4 codes16(uint32_t at, int imm) const {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(c, (int)crow + imm, (int)at, 0));
+    }
+    __device__ __forceinline__ u32x4 scale16(uint32_t at) const {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(s, (int)srow, (int)at, 0));
+    }
+    __device__ __forceinline__ uint2 scale8(uint32_t at) const {
+        return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(s, (int)srow, (int)at, 0));
+    }
+    __device__ __forceinline__ uint32_t scale4(uint32_t at) const {
+        return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(s, (int)srow, (int)at, 0);
+    }
+    __device__ __forceinline__ uint32_t scale1(uint32_t at) const {     // at differs by lane
+        return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(s, (int)(srow + at), 0, 0);
+    }
+};
+// ODD chunks differ by lane: the byte of the row goes into the lane's offset
+struct WSrcOdd : WSrc {
+    __device__ __forceinline__ u32x4 codes16(uint32_t at, int imm) const {
+        return __builtin_bit_cast(u32x4,
+                                  __builtin_amdgcn_raw_buffer_load_b128(c, (int)(crow + at) + imm, 0, 0));
     }
 };
 
@@ -167,6 +197,20 @@ struct Tile {
 struct XRow {
     const uint8_t* codes;
     const uint8_t* scales;
+    __device__ __forceinline__ u32x4 codes16(uint32_t at, int imm) const {
+        return *reinterpret_cast<const u32x4*>(codes + at + imm);
+    }
+    __device__ __forceinline__ u32x4 scale16(uint32_t at) const {
+        return *reinterpret_cast<const u32x4_a4*>(scales + at);
+    }
+    __device__ __forceinline__ uint2 scale8(uint32_t at) const {
+        const u32x2_a4 v = *reinterpret_cast<const u32x2_a4*>(scales + at);
+        return make_uint2(v.x, v.y);
+    }
+    __device__ __forceinline__ uint32_t scale4(uint32_t at) const {
+        return *reinterpret_cast<const uint32_t*>(scales + at);
+    }
+    __device__ __forceinline__ uint32_t scale1(uint32_t at) const { return scales[at]; }
 };
 template <int F>
 __device__ __forceinline__ XRow x_row(const uint8_t* codes, const uint8_t* scales, int64_t row, int64_t K,
@@ -186,6 +230,16 @@ struct Unit {
     int rows, s0, s1, id;
 };
 
+// Steps [s0, s1) of wave's share of `steps` steps among `waves`, in whole groups
+// of kSteps where FULL.
+template <int kSteps, bool FULL>
+__device__ __forceinline__ void share(int steps, int wave, int waves, int& s0, int& s1) {
+    constexpr int g = FULL ? kSteps : 1;
+    const int n = steps / g;
+    s0 = wave * n / waves * g;
+    s1 = (wave + 1) * n / waves * g;
+}
+
 // The products of all of a wave's units: first(u) gives the first one, next(u)
 // the one after u (false: no more), xrow(u, n) a lane's activation row of tile n
 // (rows past u.rows: any valid one, their products go nowhere), ending(u) is
@@ -197,13 +251,13 @@ struct Unit {
 // too (from the L2), for as many of their tiles as the registers hold, skipping
 // tiles without rows.  (Issued after them, the rows waited for the next weights
 // and the stream lost its overlap.)
-template <int WF, int XF, int RT, int NT, int kSteps, bool ODD, class First, class Next, class XRowOf,
-          class Ending, class Done>
+template <int WF, int XF, int RT, int NT, int kSteps, bool FULL, bool ODD, class First, class Next,
+          class XRowOf, class Ending, class Done>
 __device__ __forceinline__ void stream(int64_t K, int lane, First first, Next next, XRowOf xrow,
                                        Ending ending, Done done) {
     using U = Unit<RT>;
-    using TW = Tile<WF, kSteps, ODD>;
-    using TX = Tile<XF, kSteps, ODD>;
+    using TW = Tile<WF, kSteps, FULL, ODD>;
+    using TX = Tile<XF, kSteps, FULL, ODD>;
     // registers: two groups of weights, the sums, and kFirst tiles of X, of the
     // 256 that two waves a SIMD have
     constexpr int kHeld = 2 * RT * kSteps * (4 * TW::kL + 1) + 4 * RT * NT, kX = kSteps * (4 * TX::kL + 1);
@@ -212,8 +266,6 @@ __device__ __forceinline__ void stream(int64_t K, int lane, First first, Next ne
     struct Group {
         TW w[RT];
     };
-    const LaneRow lr = lane_row<WF>(K, lane);
-    const LaneRow own{0u, 0u, lane >> 4};      // x rows are the lanes' own
     const int q = lane >> 4;
     v4f acc[RT][NT];
     auto clear = [&]() {
@@ -222,32 +274,40 @@ __device__ __forceinline__ void stream(int64_t K, int lane, First first, Next ne
 #pragma unroll
             for (int n = 0; n < NT; ++n) acc[t][n] = v4f{0.f, 0.f, 0.f, 0.f};
     };
-    auto load = [&](Group& g, const U& u, int step) {
+    auto load = [&](Group& g, const U& u, int step, bool live) {
 #pragma unroll
-        for (int t = 0; t < RT; ++t) g.w[t].load(u.wc[t], u.ws[t], lr, step, u.s1, K);
+        for (int t = 0; t < RT; ++t) {
+            const WSrc src = WSrc::of<WF>(u.wc[t], u.ws[t], K, live, lane);
+            if constexpr (ODD) g.w[t].load(WSrcOdd{src}, step, u.s1, K, q);
+            else g.w[t].load(src, step, u.s1, K, q);
+        }
     };
     auto mac = [&](const Group& g, const TX& x, auto nc, const U& u, int step) {
         constexpr int n = decltype(nc)::value;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
-            if (i == 0 || step + i < u.s1) {
+            if (FULL || i == 0 || step + i < u.s1) {
+                u32x4 xc[TX::kL];
+                x.codes(xc, i, step + i, K, q);
+                const uint32_t xs = x.scale(i, step + i, K, q);
 #pragma unroll
-                for (int t = 0; t < RT; ++t)
-                    acc[t][n] = mac_step<WF, XF>(acc[t][n], g.w[t].c + i * TW::kL, g.w[t].scale(i, q),
-                                                 x.c + i * TX::kL, x.scale(i, q));
+                for (int t = 0; t < RT; ++t) {
+                    u32x4 wc[TW::kL];
+                    g.w[t].codes(wc, i, step + i, K, q);
+                    acc[t][n] = mac_step<WF, XF>(acc[t][n], wc, g.w[t].scale(i, step + i, K, q), xc, xs);
+                }
             }
     };
     TX xs[kFirst];
-    auto load_x = [&](TX& x, const U& u, int n, int step) {
-        const XRow r = xrow(u, n);
-        x.load(r.codes, r.scales, own, step, u.s1, K);
-    };
+    auto load_x = [&](TX& x, const U& u, int n, int step) { x.load(xrow(u, n), step, u.s1, K, q); };
     // f(integral_constant<n>) for the tiles A <= n < B that have rows
     auto tiles = [&](auto ac, auto bc, const U& u, auto&& f) {
         auto one = [&](auto nc) {
             constexpr int n = decltype(nc)::value;
-            if constexpr (n >= decltype(ac)::value && n < decltype(bc)::value)
-                if (n == 0 || n * 16 < u.rows) f(nc);
+            if constexpr (n >= decltype(ac)::value && n < decltype(bc)::value) {
+                if constexpr (n == 0) f(nc);
+                else if (n * 16 < u.rows) f(nc);
+            }
         };
         one(std::integral_constant<int, 0>{});
         one(std::integral_constant<int, 1>{});
@@ -262,35 +322,46 @@ __device__ __forceinline__ void stream(int64_t K, int lane, First first, Next ne
     int step = u.s0;
     Group a, b;
     clear();
-    load(a, u, step);
-    // one turn: the next group's loads, then this one's products
-    auto turn = [&](Group& mine, Group& other) -> bool {
+    load(a, u, step, true);
+    // One turn: the next group's loads (of no bytes after the last one), then this
+    // one's products.  Two turns make a round, the second one without work where
+    // the groups are odd in number: a way out between them would give the compiler
+    // a path from a turn to itself, on which it would wait for the loads in flight.
+    bool live = true;
+    auto turn = [&](Group& mine, Group& other) {
         U v = u;
         int vstep = step + kSteps;
-        bool more = true;
-        if (vstep >= u.s1) {
+        bool more = live;
+        if (live && vstep >= u.s1) {
             more = next(v);
             vstep = v.s0;
+            ending(u);
         }
-        if (step + kSteps >= u.s1) ending(u);
-        tiles(k0, kF, u, [&](auto nc) { load_x(xs[decltype(nc)::value], u, decltype(nc)::value, step); });
-        if (more) load(other, v, vstep);
-        tiles(k0, kF, u, [&](auto nc) { mac(mine, xs[decltype(nc)::value], nc, u, step); });
-        tiles(kF, kN, u, [&](auto nc) {
-            TX x;
-            load_x(x, u, decltype(nc)::value, step);
-            mac(mine, x, nc, u, step);
-        });
-        if (step + kSteps >= u.s1) {
-            done(acc, u);
-            clear();
+        if (live)
+            tiles(k0, kF, u, [&](auto nc) { load_x(xs[decltype(nc)::value], u, decltype(nc)::value, step); });
+        __builtin_amdgcn_sched_barrier(0);       // loads in this order, products after them
+        load(other, v, vstep, more);
+        __builtin_amdgcn_sched_barrier(0);
+        if (live) {
+            tiles(k0, kF, u, [&](auto nc) { mac(mine, xs[decltype(nc)::value], nc, u, step); });
+            tiles(kF, kN, u, [&](auto nc) {
+                TX x;
+                load_x(x, u, decltype(nc)::value, step);
+                mac(mine, x, nc, u, step);
+            });
+            if (step + kSteps >= u.s1) {
+                done(acc, u);
+                clear();
+            }
         }
         u = v;
         step = vstep;
-        return more;
+        live = __builtin_amdgcn_readfirstlane((int)more);
     };
-    while (turn(a, b) && turn(b, a)) {
-    }
+    do {
+        turn(a, b);
+        turn(b, a);
+    } while (live);
 }
 
 }  // namespace few

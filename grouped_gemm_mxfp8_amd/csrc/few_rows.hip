@@ -17,6 +17,7 @@
 #include <stdint.h>
 
 #include "few_rows.h"
+#include "gemm_device.h"
 #include "internal.h"
 #include "mx_device.h"
 
@@ -24,11 +25,6 @@ namespace mx {
 namespace {
 
 using namespace few;
-
-__device__ __forceinline__ int64_t uni64(int64_t v) {
-    const uint32_t lo = (uint32_t)uni((int)(uint32_t)v), hi = (uint32_t)uni((int)(uint32_t)((uint64_t)v >> 32));
-    return (int64_t)(((uint64_t)hi << 32) | lo);
-}
 
 // ---- GroupedLinear, few rows an expert --------------------------------------
 
@@ -47,7 +43,7 @@ struct LinearArgs {
 // A workgroup's units: 64 columns of y for up to 16 NT rows of one expert, the
 // four waves a quarter of K each.  Units run over (expert with rows, column
 // block), and over an expert's row chunks within one.
-template <int XF, int NT, int kSteps, bool ODD>
+template <int XF, int NT, int kSteps, bool FULL, bool ODD>
 __global__ void __launch_bounds__(64 * kLinWaves, 2)
 linear4_few_kernel(LinearArgs p) {
     __shared__ __attribute__((aligned(16))) float parts[2][kLinWaves * 1024];
@@ -79,10 +75,10 @@ linear4_few_kernel(LinearArgs p) {
     const int ncol = (int)((p.N + kLinRows - 1) / kLinRows);
     const int64_t units = (int64_t)uni(s_count) * ncol;
     const int steps = (int)((p.K + 127) / 128);
-    // waves past the number of steps repeat step 0; their sums are not added
-    const int waves = min(kLinWaves, steps);
-    const int s0 = wave < waves ? wave * steps / waves : 0;
-    const int s1 = wave < waves ? (wave + 1) * steps / waves : 1;
+    // waves past the number of groups repeat the first one; their sums are not added
+    const int waves = min(kLinWaves, FULL ? steps / kSteps : steps);
+    int s0, s1;
+    share<kSteps, FULL>(steps, wave < waves ? wave : 0, waves, s0, s1);
     using U = Unit<4>;
     auto place = [&](U& u, int id, int64_t m0) -> bool {      // rows from m0, or the expert's first (m0 < 0)
         if (id >= units) return false;
@@ -106,7 +102,7 @@ linear4_few_kernel(LinearArgs p) {
     };
     int turn = 0;
     float scale[NT];                 // row scale of this thread's token in done
-    stream<kFp4, XF, 4, NT, kSteps, ODD>(
+    stream<kFp4, XF, 4, NT, kSteps, FULL, ODD>(
         p.K, lane, [&](U& u) { return place(u, blockIdx.x, -1); },
         [&](U& u) {
             const int64_t hi = uni64(s_hi[u.id / ncol]);
@@ -134,7 +130,7 @@ linear4_few_kernel(LinearArgs p) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     *reinterpret_cast<v4f*>(part + ((wave * 4 + t) * 64 + lane) * 4) = acc[t][n];
-                __syncthreads();
+                lds_barrier();       // (__syncthreads would wait for the weights in flight)
                 const int tok = tid >> 4, c4 = tid & 15;          // columns n0 + 4 c4 .. + 3
                 const int at = ((c4 >> 2) * 64 + (c4 & 3) * 16 + tok) * 4;
                 v4f s = *reinterpret_cast<const v4f*>(part + at);
@@ -351,7 +347,7 @@ __device__ __forceinline__ PlanLds read_plan(const LayerArgs& p, uint8_t* smem) 
 // A workgroup's units: 32 columns of z (tiles 0, 1: their gate rows of W1; 2, 3:
 // the up rows) for up to 16 NT rows of one routed expert, the four waves a
 // quarter of H each.
-template <int WF, int NT, int kSteps>
+template <int WF, int NT, int kSteps, bool FULL>
 __global__ void __launch_bounds__(64 * kGuWaves, 2)
 layer_gate_up_kernel(LayerArgs p) {
     constexpr int XF = WF == kBf16 ? kBf16 : kFp8;
@@ -361,10 +357,10 @@ layer_gate_up_kernel(LayerArgs p) {
     const PlanLds plan = read_plan(p, smem);
     const int ncol = (int)(p.F / 32), units = plan.n_act * ncol;
     const int steps = (int)(p.H / 128);
-    // waves past the number of steps repeat step 0; their sums are not added
-    const int waves = min(kGuWaves, steps);
-    const int s0 = wave < waves ? wave * steps / waves : 0;
-    const int s1 = wave < waves ? (wave + 1) * steps / waves : 1;
+    // waves past the number of groups repeat the first one; their sums are not added
+    const int waves = min(kGuWaves, FULL ? steps / kSteps : steps);
+    int s0, s1;
+    share<kSteps, FULL>(steps, wave < waves ? wave : 0, waves, s0, s1);
     const int64_t wb = row_bytes(WF, p.H), sb = p.H / 32;
     using U = Unit<4>;
     auto place = [&](U& u, int id, int c0) -> bool {       // the expert's rows from its c0-th
@@ -387,7 +383,7 @@ layer_gate_up_kernel(LayerArgs p) {
         return true;
     };
     int turn = 0;
-    stream<WF, XF, 4, NT, kSteps, false>(
+    stream<WF, XF, 4, NT, kSteps, FULL, false>(
         p.H, lane, [&](U& u) { return place(u, blockIdx.x, 0); },
         [&](U& u) {
             const int4 ex = plan.act[u.id / ncol];
@@ -418,7 +414,7 @@ layer_gate_up_kernel(LayerArgs p) {
                 const bool live = row < u.rows;
                 const int64_t zrow = u.row0 + row;
                 const float r = live ? plan.r[zrow] : 0.f;
-                __syncthreads();
+                lds_barrier();
                 const int at = ((c >> 4) * 64 + ((c & 15) >> 2) * 16 + tok) * 4 + (c & 3);
                 float g[2] = {0.f, 0.f}, up[2] = {0.f, 0.f};
 #pragma unroll
@@ -480,7 +476,7 @@ constexpr int down_tiles(bool bf16, int64_t T) {
 // (Adding them in the last workgroup to arrive took six times as long: the
 // fences that such a hand-over needs write the XCD's L2 back, 0.3 us each.)
 // TMAX: bound of T that sizes the sums.
-template <int WF, int NT, int kSteps, int RT, int TMAX>
+template <int WF, int NT, int kSteps, bool FULL, int RT, int TMAX>
 __global__ void __launch_bounds__(64 * kDnWaves, 2)
 layer_down_kernel(LayerArgs p) {
     constexpr int XF = WF == kBf16 ? kBf16 : kFp8;
@@ -496,7 +492,7 @@ layer_down_kernel(LayerArgs p) {
     const PlanLds plan = read_plan(p, smem);
     const int steps = (int)(p.F / 128);
     // parts of F per expert, so that every wave has work with few experts
-    const int parts = max(1, min((steps + kSteps - 1) / kSteps,
+    const int parts = max(1, min(FULL ? steps / kSteps : (steps + kSteps - 1) / kSteps,
                                  (2 * waves + plan.n_act - 1) / max(plan.n_act, 1)));
     const int units = plan.n_act * parts;
     const int64_t wb = row_bytes(WF, p.F), sb = p.F / 32;
@@ -507,8 +503,7 @@ layer_down_kernel(LayerArgs p) {
         const int4 ex = plan.act[a];
         u.row0 = uni(ex.y) + c0;
         u.rows = min(16 * NT, uni(ex.z) - c0);
-        u.s0 = c * steps / parts;
-        u.s1 = (c + 1) * steps / parts;
+        share<kSteps, FULL>(steps, c, parts, u.s0, u.s1);
         u.id = id;
         const int64_t r = (int64_t)uni(ex.x) * p.H + h0;
 #pragma unroll
@@ -518,7 +513,7 @@ layer_down_kernel(LayerArgs p) {
         }
         return true;
     };
-    stream<WF, XF, RT, NT, kSteps, false>(
+    stream<WF, XF, RT, NT, kSteps, FULL, false>(
         p.F, lane, [&](U& u) { return place(u, part * kDnWaves + wave, 0); },
         [&](U& u) {
             const int4 ex = plan.act[u.id / parts];
@@ -581,12 +576,20 @@ hipError_t launch_layer_rows(const LayerArgs& p, hipStream_t s) {
     const size_t lds = plan_lds_bytes(p);
     const int64_t units = experts * (p.F / 32);
     const int64_t fit = 2 * device_cu_count();
-    hipLaunchKernelGGL((layer_gate_up_kernel<WF, NT, gs>), dim3((unsigned)(units < fit ? units : fit)),
-                       dim3(64 * kGuWaves), lds, s, p);
+    auto gate_up = [&](auto full) {
+        hipLaunchKernelGGL((layer_gate_up_kernel<WF, NT, gs, decltype(full)::value>),
+                           dim3((unsigned)(units < fit ? units : fit)), dim3(64 * kGuWaves), lds, s, p);
+    };
+    if (p.H / 128 % gs == 0) gate_up(std::true_type{});
+    else gate_up(std::false_type{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((layer_down_kernel<WF, NT, ds, rt, TMAX>), dim3((unsigned)(p.H / (16 * rt) * p.split)),
-                       dim3(64 * kDnWaves), lds, s, p);
+    auto down = [&](auto full) {
+        hipLaunchKernelGGL((layer_down_kernel<WF, NT, ds, decltype(full)::value, rt, TMAX>),
+                           dim3((unsigned)(p.H / (16 * rt) * p.split)), dim3(64 * kDnWaves), lds, s, p);
+    };
+    if (p.F / 128 % ds == 0) down(std::true_type{});
+    else down(std::false_type{});
     if (p.split > 1)
         hipLaunchKernelGGL(layer_sum_kernel, dim3((unsigned)((p.T * p.H / 8 + 255) / 256)), dim3(256), 0, s, p);
     return hipGetLastError();
@@ -605,8 +608,15 @@ void launch_few(const LinearArgs& a, int64_t M, hipStream_t s) {
     const int64_t units = (M < a.G ? M : a.G) * ((a.N + kLinRows - 1) / kLinRows);
     const int64_t fit = 2 * device_cu_count();
     const dim3 grid((unsigned)(units < fit ? units : fit));
-    if (M <= 16) hipLaunchKernelGGL((linear4_few_kernel<XF, 1, 4, ODD>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((linear4_few_kernel<XF, 4, 2, ODD>), grid, dim3(256), 0, s, a);
+    auto go = [&](auto nt, auto ks) {
+        constexpr int NT = decltype(nt)::value, KS = decltype(ks)::value;
+        if (!ODD && a.K / 128 % KS == 0)
+            hipLaunchKernelGGL((linear4_few_kernel<XF, NT, KS, !ODD, ODD>), grid, dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL((linear4_few_kernel<XF, NT, KS, false, ODD>), grid, dim3(256), 0, s, a);
+    };
+    if (M <= 16) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
+    else go(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
 }
 
 }  // namespace
