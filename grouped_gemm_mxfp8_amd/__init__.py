@@ -9,7 +9,6 @@ functions raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 import os
@@ -118,8 +117,27 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without making a Stream object (2 us a call), where
+# torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream(dev):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    return ctypes.c_void_p(_raw_stream(dev.index))
+
+
+def _launch(name, dev, *args):
+    """Calls entry point ``name`` on ``dev`` and its current stream (the last
+    argument); raises MxError on a non-zero status.  Addresses are plain ints."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev.index))
+    if st != 0:
+        raise MxError(name, st, last_error())
 
 
 def _need(t, dtype, name, dev=None):
@@ -199,12 +217,6 @@ class Mx4Tensor:
     scales: torch.Tensor
 
 
-def _on(dev):
-    """Makes ``dev`` the current device for a library call (a no-op where it is)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else \
-        torch.cuda.device(dev)
-
-
 def mxfp4_quantize(x: torch.Tensor, rowwise: bool = True, colwise: bool = False):
     """Block-quantize bf16 ``x`` ([R, C] or [batch, R, C]) to MXFP4.
 
@@ -212,36 +224,29 @@ def mxfp4_quantize(x: torch.Tensor, rowwise: bool = True, colwise: bool = False)
     ``col`` (the transposed copy, blocks along R: Mx4Tensor [.., C, R/2] /
     [.., C, R/32], R a multiple of 32).  C is a multiple of 32."""
     _need(x, torch.bfloat16, "x")
-    dev = x.device
-    if x.dim() == 2:
-        (R, C), lead, batch = x.shape, (), 1
-    elif x.dim() == 3:
-        batch, R, C = x.shape
-        lead = (batch,)
-    else:
+    dev, shape = x.device, x.shape
+    if len(shape) not in (2, 3):
         raise ValueError("x must be 2-D or 3-D")
-    if batch == 0:
-        raise ValueError("x has no matrices")
+    R, C = shape[-2:]
+    lead = shape[:-2]
+    batch = lead[0] if lead else 1
+    if C % BLOCK or (colwise and R % BLOCK):
+        raise ValueError(f"C (and R of a columnwise copy) must be multiples of {BLOCK}")
+    if batch == 0 or not (rowwise or colwise):
+        raise ValueError("x has no matrices" if batch == 0 else
+                         "rowwise or colwise must be requested")
     out = {}
-    rc = rs = cc = cs = None
+    rc = rs = cc = cs = 0
     if rowwise:
-        rc = torch.empty((*lead, R, C // 2), dtype=torch.uint8, device=dev)
-        rs = torch.empty((*lead, R, C // BLOCK), dtype=torch.uint8, device=dev)
-        out["row"] = Mx4Tensor(rc, rs)
+        q = Mx4Tensor(torch.empty((*lead, R, C // 2), dtype=torch.uint8, device=dev),
+                      torch.empty((*lead, R, C // BLOCK), dtype=torch.uint8, device=dev))
+        out["row"], rc, rs = q, q.codes.data_ptr(), q.scales.data_ptr()
     if colwise:
-        cc = torch.empty((*lead, C, R // 2), dtype=torch.uint8, device=dev)
-        cs = torch.empty((*lead, C, R // BLOCK), dtype=torch.uint8, device=dev)
-        out["col"] = Mx4Tensor(cc, cs)
-    if x.numel() == 0:           # nothing to launch (empty tensors have no address)
-        if not out:
-            raise ValueError("rowwise or colwise must be requested")
-        if C % BLOCK or (colwise and R % BLOCK):
-            raise ValueError(f"C (and R of a columnwise copy) must be multiples of {BLOCK}")
-        return out
-    with _on(dev):
-        st = lib().mxfp4_quantize(_ptr(x), batch, R, C, _ptr(rc), _ptr(rs), _ptr(cc), _ptr(cs),
-                                  _stream(dev))
-    _check("mxfp4_quantize", st)
+        q = Mx4Tensor(torch.empty((*lead, C, R // 2), dtype=torch.uint8, device=dev),
+                      torch.empty((*lead, C, R // BLOCK), dtype=torch.uint8, device=dev))
+        out["col"], cc, cs = q, q.codes.data_ptr(), q.scales.data_ptr()
+    if x.numel():                # (empty tensors have no address)
+        _launch("mxfp4_quantize", dev, x.data_ptr(), batch, R, C, rc, rs, cc, cs)
     return out
 
 
@@ -273,10 +278,8 @@ def mxfp4_dequantize(q: Mx4Tensor) -> torch.Tensor:
     dev = q.codes.device
     y = torch.empty((*q.codes.shape[:-1], C), dtype=torch.bfloat16, device=dev)
     if y.numel():
-        with _on(dev):
-            st = lib().mxfp4_dequantize(_ptr(q.codes), _ptr(q.scales), y.numel() // C, C, _ptr(y),
-                                        _stream(dev))
-        _check("mxfp4_dequantize", st)
+        _launch("mxfp4_dequantize", dev, q.codes.data_ptr(), q.scales.data_ptr(), y.numel() // C, C,
+                y.data_ptr())
     return y
 
 
@@ -347,13 +350,10 @@ def _linear_mxfp4(x, offsets, w: Mx4Tensor, row_scale):
         if tuple(row_scale.shape) != (M,):
             raise ValueError("row_scale must be [M]")
     y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    if M == 0:
-        return y
-    with _on(dev):
-        st = lib().grouped_linear_fwd(dtype, _ptr(x.codes), _ptr(x.scales), _ptr(offsets), E, M,
-                                      _ptr(w.codes), _ptr(w.scales), N, K, _ptr(row_scale),
-                                      _ptr(y), _stream(dev))
-    _check("grouped_linear_fwd", st)
+    if M:
+        _launch("grouped_linear_fwd", dev, dtype, x.codes.data_ptr(), x.scales.data_ptr(),
+                offsets.data_ptr(), E, M, w.codes.data_ptr(), w.scales.data_ptr(), N, K,
+                0 if row_scale is None else row_scale.data_ptr(), y.data_ptr())
     return y
 
 
@@ -800,10 +800,9 @@ def moe_layer_fwd(x: torch.Tensor, logits: torch.Tensor, w1, w2, k: int,
         ws = torch.empty(nws, dtype=torch.uint8, device=dev)
     else:
         _need(ws, torch.uint8, "ws", dev)
-    with _on(dev):
-        st = L.moe_layer_fwd(d1, _ptr(x), _ptr(logits), T, E, k, H, F, _ptr(t1), _ptr(s1),
-                             _ptr(t2), _ptr(s2), _ptr(out), _ptr(ws), nws, _stream(dev))
-    _check("moe_layer_fwd", st)
+    _launch("moe_layer_fwd", dev, d1, x.data_ptr(), logits.data_ptr(), T, E, k, H, F, t1.data_ptr(),
+            0 if s1 is None else s1.data_ptr(), t2.data_ptr(), 0 if s2 is None else s2.data_ptr(),
+            out.data_ptr(), ws.data_ptr(), nws)
     return out
 
 

@@ -163,6 +163,20 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
+// Reductions over a wave's 64 lanes, every lane with the result: DPP within rows
+// of 16, then swaps 16 and 32 lanes apart (no LDS traffic, unlike a shuffle).
+template <class Op>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, Op op) {
+    v = op(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));     // lanes ^ 1
+    v = op(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));     // lanes ^ 2
+    v = op(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x124, 0xF, 0xF, false));    // row_ror:4
+    v = op(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, false));    // row_ror:8
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = op(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return op(b[0], b[1]);
+}
+
 // Workgroup 0 of layer_prep.  LDS: the selected experts of each token as bits,
 // each expert's rows, and each token's softmax terms.  W: 64-expert words per
 // token that the registers hold (1 for E <= 64, else the largest).
@@ -209,15 +223,15 @@ __device__ void layer_plan(const float* __restrict__ logits, int T, int E, int k
             if (lane == i) mine = b;
             if (on[i]) top = max(top, key[i]);
         }
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+        top = wave_reduce(top, [](uint32_t a, uint32_t b) { return max(a, b); });
         const float m = key_logit(top);
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < W; ++i)
             if (on[i]) sum += expf(key_logit(key[i]) - m);
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+        sum = __uint_as_float(wave_reduce(__float_as_uint(sum), [](uint32_t a, uint32_t b) {
+            return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+        }));
         if (lane < words) sel[t * words + lane] = mine;
         if (lane == 0) {
             mx[t] = m;
@@ -225,11 +239,15 @@ __device__ void layer_plan(const float* __restrict__ logits, int T, int E, int k
         }
     }
     __syncthreads();
-    // rows of each expert
-    for (int e = tid; e < E; e += kPrepThreads) {
+    // the tokens of an expert as bits, a wave for each expert: lane = token
+    auto tokens = [&](int e, int t0) -> uint64_t {
+        const int t = t0 + lane;
+        return __ballot(t < T && (sel[t * words + (e >> 6)] >> (e & 63) & 1));
+    };
+    for (int e = wave; e < E; e += kPrepThreads / 64) {
         int n = 0;
-        for (int t = 0; t < T; ++t) n += (int)(sel[t * words + (e >> 6)] >> (e & 63) & 1);
-        cnt[e] = n;
+        for (int t0 = 0; t0 < T; t0 += 64) n += __popcll(tokens(e, t0));
+        if (lane == 0) cnt[e] = n;
     }
     __syncthreads();
     // wave 0: first row of each expert and the list of routed experts
@@ -255,17 +273,20 @@ __device__ void layer_plan(const float* __restrict__ logits, int T, int E, int k
         if (lane == 0) *plan.n_act = act;
     }
     __syncthreads();
-    // (token, expert) pairs to their rows: tokens ascend within an expert
-    for (int i = tid; i < T * E; i += kPrepThreads) {
-        const int t = i / E, e = i - t * E;
-        const int wd = e >> 6, sh = e & 63;
-        if (!(sel[t * words + wd] >> sh & 1)) continue;
-        int before = 0;
-        for (int u = 0; u < t; ++u) before += (int)(sel[u * words + wd] >> sh & 1);
-        const int row = cnt[e] + before;
-        plan.tok[row] = t;
-        const float v = key_logit(logit_key(logits[(int64_t)t * E + e]));
-        plan.r[row] = expf(v - mx[t]) * inv[t];
+    // rows: an expert's tokens in order, with their routing weights
+    for (int e = wave; e < E; e += kPrepThreads / 64) {
+        int row = cnt[e];
+        for (int t0 = 0; t0 < T; t0 += 64) {
+            const uint64_t b = tokens(e, t0);
+            const int t = t0 + lane;
+            if (b >> lane & 1) {
+                const int at = row + __popcll(b & ((1ull << lane) - 1));
+                plan.tok[at] = t;
+                const float v = key_logit(logit_key(logits[(int64_t)t * E + e]));
+                plan.r[at] = expf(v - mx[t]) * inv[t];
+            }
+            row += __popcll(b);
+        }
     }
 }
 

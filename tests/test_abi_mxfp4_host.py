@@ -127,7 +127,8 @@ def test_layer_workspace_bytes(mxlib):
     f = mxlib.moe_layer_ws_bytes
     T, E, k, H, F = 64, 64, 8, 2048, 1408
     need = T * H * 33 // 32 + T * k * F * 33 // 32 + T * k * 8 + E * 16
-    assert need <= f(FP4, T, E, k, H, F) <= need + 16 * 256
+    parts = 8 * T * H * 4          # at most eight partial sums of the output
+    assert need <= f(FP4, T, E, k, H, F) <= need + parts + 16 * 256
     assert f(FP4, T, E, k, H, F) == f(FP8, T, E, k, H, F)
     assert T * k * F * 2 <= f(BF16, T, E, k, H, F)
     assert f(FP4, 0, E, k, H, F) > 0
