@@ -189,21 +189,33 @@ __device__ void layer_plan(const float* __restrict__ logits, int T, int E, int k
     int* cnt = reinterpret_cast<int*>(sel + (int64_t)T * words);         // [E] rows, then first rows
     float* mx = reinterpret_cast<float*>(cnt + E);                       // [T] largest logit
     float* inv = mx + T;                                                 // [T] 1 / sum of exponentials
-    for (int t = wave; t < T; t += kPrepThreads / 64) {
-        uint32_t key[W];
+    auto read = [&](float (&v)[W], int t) {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             const int e = lane + 64 * i;
-            key[i] = e < E ? logit_key(logits[(int64_t)t * E + e]) : 0u;
+            v[i] = t < T && e < E ? logits[(int64_t)t * E + e] : -__builtin_inff();
         }
-        // th: the largest value that at least k keys reach (0 if fewer routed)
+    };
+    float ahead[W];                      // the next token's logits
+    read(ahead, wave);
+    for (int t = wave; t < T; t += kPrepThreads / 64) {
+        uint32_t key[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) key[i] = logit_key(ahead[i]);
+        read(ahead, t + kPrepThreads / 64);
+        // th: the largest value that at least k keys reach (0 if fewer routed), or,
+        // as soon as a value splits off exactly k keys, the one below it
         uint32_t th = 0;
         for (int bit = 31; bit >= 0; --bit) {
             const uint32_t cand = th | (1u << bit);
             int n = 0;
 #pragma unroll
             for (int i = 0; i < W; ++i) n += __popcll(__ballot(key[i] >= cand));
-            if (n >= k) th = cand;
+            if (n == k) {
+                th = cand - 1;
+                break;
+            }
+            if (n > k) th = cand;
         }
         int above = 0;
 #pragma unroll
@@ -239,12 +251,27 @@ __device__ void layer_plan(const float* __restrict__ logits, int T, int E, int k
         }
     }
     __syncthreads();
-    // the tokens of an expert as bits, a wave for each expert: lane = token
+    // An expert's tokens: by one thread for each expert, token by token (about 40
+    // cycles each), or by one of the 16 waves, 64 tokens in a ballot (about 150):
+    // the first where 4 T < E for every 64 tokens.
+    const bool by_thread = 4 * T < E * ((T + 63) / 64);
+    auto routed = [&](int t, int e) { return (sel[t * words + (e >> 6)] >> (e & 63) & 1) != 0; };
+    auto place = [&](int row, int t, int e) {
+        plan.tok[row] = t;
+        const float v = key_logit(logit_key(logits[(int64_t)t * E + e]));
+        plan.r[row] = expf(v - mx[t]) * inv[t];
+    };
     auto tokens = [&](int e, int t0) -> uint64_t {
         const int t = t0 + lane;
-        return __ballot(t < T && (sel[t * words + (e >> 6)] >> (e & 63) & 1));
+        return __ballot(t < T && routed(t, e));
     };
-    for (int e = wave; e < E; e += kPrepThreads / 64) {
+    if (by_thread) {
+        for (int e = tid; e < E; e += kPrepThreads) {
+            int n = 0;
+            for (int t = 0; t < T; ++t) n += routed(t, e);
+            cnt[e] = n;
+        }
+    } else for (int e = wave; e < E; e += kPrepThreads / 64) {
         int n = 0;
         for (int t0 = 0; t0 < T; t0 += 64) n += __popcll(tokens(e, t0));
         if (lane == 0) cnt[e] = n;
@@ -274,17 +301,18 @@ __device__ void layer_plan(const float* __restrict__ logits, int T, int E, int k
     }
     __syncthreads();
     // rows: an expert's tokens in order, with their routing weights
-    for (int e = wave; e < E; e += kPrepThreads / 64) {
+    if (by_thread) {
+        for (int e = tid; e < E; e += kPrepThreads) {
+            int row = cnt[e];
+            for (int t = 0; t < T; ++t)
+                if (routed(t, e)) place(row++, t, e);
+        }
+    } else for (int e = wave; e < E; e += kPrepThreads / 64) {
         int row = cnt[e];
         for (int t0 = 0; t0 < T; t0 += 64) {
             const uint64_t b = tokens(e, t0);
             const int t = t0 + lane;
-            if (b >> lane & 1) {
-                const int at = row + __popcll(b & ((1ull << lane) - 1));
-                plan.tok[at] = t;
-                const float v = key_logit(logit_key(logits[(int64_t)t * E + e]));
-                plan.r[at] = expf(v - mx[t]) * inv[t];
-            }
+            if (b >> lane & 1) place(row + __popcll(b & ((1ull << lane) - 1)), t, e);
             row += __popcll(b);
         }
     }
