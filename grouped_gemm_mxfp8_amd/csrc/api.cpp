@@ -1234,7 +1234,7 @@ LayerWs layer_ws(int32_t wdtype, int64_t T, int32_t E, int32_t k, int64_t H, int
     L.xqs = c.take(mxw ? (size_t)(T * H / 32) : 0);
     L.z = c.take((size_t)(rows * F) * (mxw ? 1 : 2));
     L.zs = c.take(mxw ? (size_t)(rows * F / 32) : 0);
-    L.split = mx::layer_split(!mxw, T, H);
+    L.split = mx::layer_split(!mxw, T, k, E, H);
     L.parts = c.take(L.split > 1 ? (size_t)(L.split * T * H) * 4 : 0);
     L.total = c.off;
     return L;

@@ -178,7 +178,7 @@ __device__ __forceinline__ uint32_t wave_reduce(uint32_t v, Op op) {
 }
 
 // Workgroup 0 of layer_prep.  LDS: the selected experts of each token as bits,
-// each expert's rows, and each token's softmax terms.  W: 64-expert words per
+// each expert's rows, and each token's routing weights.  W: 64-expert words per
 // token that the registers hold (1 for E <= 64, else the largest).
 template <int W>
 __device__ void layer_plan(const float* __restrict__ logits, int T, int E, int k, const LayerPlan& plan,
@@ -187,8 +187,7 @@ __device__ void layer_plan(const float* __restrict__ logits, int T, int E, int k
     const int words = (E + 63) / 64;                                     // 64-expert words per token
     uint64_t* sel = reinterpret_cast<uint64_t*>(smem);                   // [T][words]
     int* cnt = reinterpret_cast<int*>(sel + (int64_t)T * words);         // [E] rows, then first rows
-    float* mx = reinterpret_cast<float*>(cnt + E);                       // [T] largest logit
-    float* inv = mx + T;                                                 // [T] 1 / sum of exponentials
+    float* wt = reinterpret_cast<float*>(cnt + E);                       // [T][k] weights, by expert
     auto read = [&](float (&v)[W], int t) {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
@@ -237,17 +236,22 @@ __device__ void layer_plan(const float* __restrict__ logits, int T, int E, int k
         }
         top = wave_reduce(top, [](uint32_t a, uint32_t b) { return max(a, b); });
         const float m = key_logit(top);
-        float sum = 0.f;
+        float ex[W], sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (on[i]) sum += expf(key_logit(key[i]) - m);
+        for (int i = 0; i < W; ++i) {
+            ex[i] = on[i] ? expf(key_logit(key[i]) - m) : 0.f;
+            sum += ex[i];
+        }
         sum = __uint_as_float(wave_reduce(__float_as_uint(sum), [](uint32_t a, uint32_t b) {
             return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
         }));
         if (lane < words) sel[t * words + lane] = mine;
-        if (lane == 0) {
-            mx[t] = m;
-            inv[t] = 1.0f / sum;
+        int before = 0;                  // selected experts below this lane's
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const uint64_t b = __ballot(on[i]);
+            if (on[i]) wt[t * k + before + __popcll(b & ((1ull << lane) - 1))] = ex[i] / sum;
+            before += __popcll(b);
         }
     }
     __syncthreads();
@@ -258,8 +262,10 @@ __device__ void layer_plan(const float* __restrict__ logits, int T, int E, int k
     auto routed = [&](int t, int e) { return (sel[t * words + (e >> 6)] >> (e & 63) & 1) != 0; };
     auto place = [&](int row, int t, int e) {
         plan.tok[row] = t;
-        const float v = key_logit(logit_key(logits[(int64_t)t * E + e]));
-        plan.r[row] = expf(v - mx[t]) * inv[t];
+        int slot = 0;
+        for (int i = 0; i < (e >> 6); ++i) slot += __popcll(sel[t * words + i]);
+        slot += __popcll(sel[t * words + (e >> 6)] & ((1ull << (e & 63)) - 1));
+        plan.r[row] = wt[t * k + slot];
     };
     auto tokens = [&](int e, int t0) -> uint64_t {
         const int t = t0 + lane;
@@ -318,8 +324,8 @@ __device__ void layer_plan(const float* __restrict__ logits, int T, int E, int k
     }
 }
 
-size_t plan_lds(int64_t T, int E) {
-    return (size_t)(T * ((E + 63) / 64) * 8 + E * 4 + T * 8);
+size_t prep_lds(int64_t T, int E, int k) {
+    return (size_t)(T * ((E + 63) / 64) * 8 + E * 4 + T * k * 4);
 }
 
 // MXFP8 blocks of one token (H % 128 == 0), as mxfp8_quantize makes them; a
@@ -507,15 +513,24 @@ layer_gate_up_kernel(LayerArgs p) {
 constexpr int kDnWaves = 8;
 constexpr int kSplitFull = 256;    // workgroups of the down projection, one a CU
 
+// LDS of a down-projection workgroup: the plan, and its waves' sums of T tokens
+// by 16 rt columns.
+size_t down_lds(int64_t T, int k, int E, int rt) {
+    const int64_t rows = T * k, experts = E < rows ? E : rows;
+    return (size_t)(experts * 16 + rows * 8 + (int64_t)kDnWaves * T * 16 * rt * 4);
+}
+constexpr size_t kLdsBytes = 160 * 1024;
+
 // 16-row tiles of W2 a workgroup takes; z is read once for all of them, and for
 // MX weights one tile of z rows is as many bytes (MXFP4: twice) as one tile of
 // W2.  One tile: H / 16 workgroups fill the CUs and no sums of parts are left to
 // add.  Measured on 8 x (4096, 14336) MXFP4, all experts, one / two / four tiles:
 // T = 4 60 / - / - us, T = 16 92 / 68 / 67, T = 32 - / 94 / 78; 64 tokens on 64 x
-// (2048, 1408) 35 / 28 / - (four tiles of 128 tokens' sums do not fit the LDS);
-// bf16, 16 tokens: 155 / 156 / 170.
-constexpr int down_tiles(bool bf16, int64_t T) {
-    return T <= 4 || (bf16 && T <= 16) ? 1 : T <= 16 || T > 32 || bf16 ? 2 : 4;
+// (2048, 1408) 35 / 28 / -; bf16, 16 tokens: 155 / 156 / 170.
+int down_tiles(bool bf16, int64_t T, int k, int E) {
+    int rt = T <= 4 || (bf16 && T <= 16) ? 1 : T <= 16 || T > 32 || bf16 ? 2 : 4;
+    while (rt > 1 && down_lds(T, k, E, rt) > kLdsBytes) rt /= 2;
+    return rt;
 }
 
 // `split` workgroups share rows h0 .. h0 + 16 RT - 1 of every routed expert's W2.  Their
@@ -524,21 +539,20 @@ constexpr int down_tiles(bool bf16, int64_t T) {
 // With split > 1 a workgroup leaves its sums in `parts` and layer_sum adds them.
 // (Adding them in the last workgroup to arrive took six times as long: the
 // fences that such a hand-over needs write the XCD's L2 back, 0.3 us each.)
-// TMAX: bound of T that sizes the sums.
-template <int WF, int NT, int kSteps, bool FULL, int RT, int TMAX>
+template <int WF, int NT, int kSteps, bool FULL, int RT>
 __global__ void __launch_bounds__(64 * kDnWaves, 2)
 layer_down_kernel(LayerArgs p) {
     constexpr int XF = WF == kBf16 ? kBf16 : kFp8;
     constexpr int kCols = 16 * RT;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    __shared__ __attribute__((aligned(16))) float sums[kDnWaves * TMAX * 16 * RT];
     const int tid = threadIdx.x, wave = uni(tid >> 6), lane = tid & 63;
     const int64_t h0 = (int64_t)(blockIdx.x / p.split) * kCols;
     const int part = blockIdx.x % p.split, waves = kDnWaves * p.split;
     const int T = (int)p.T;
-    float* out = sums + wave * TMAX * kCols;
+    float* const sums = reinterpret_cast<float*>(smem);        // [wave][T][kCols]
+    float* const out = sums + wave * T * kCols;
     for (int i = lane; i < T * 4 * RT; i += 64) reinterpret_cast<v4f*>(out)[i] = v4f{0.f, 0.f, 0.f, 0.f};
-    const PlanLds plan = read_plan(p, smem);
+    const PlanLds plan = read_plan(p, smem + kDnWaves * T * kCols * 4);
     const int steps = (int)(p.F / 128);
     // parts of F per expert, so that every wave has work with few experts
     const int parts = max(1, min(FULL ? steps / kSteps : (steps + kSteps - 1) / kSteps,
@@ -590,7 +604,7 @@ layer_down_kernel(LayerArgs p) {
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < kDnWaves; ++v) {
-            const float2 a = *reinterpret_cast<const float2*>(sums + v * TMAX * kCols + 2 * i);
+            const float2 a = *reinterpret_cast<const float2*>(sums + v * T * kCols + 2 * i);
             s.x += a.x;
             s.y += a.y;
         }
@@ -615,41 +629,61 @@ layer_sum_kernel(LayerArgs p) {
         make_uint4(bf16x2(s[0], s[1]), bf16x2(s[2], s[3]), bf16x2(s[4], s[5]), bf16x2(s[6], s[7]));
 }
 
-template <int WF, int NT, int TMAX>
-hipError_t launch_layer_rows(const LayerArgs& p, hipStream_t s) {
-    // 16 (NT > 1: 8) loads of 16 bytes a lane and group in gate-up, 4 a tile in down
-    constexpr int L = loads_per_step(WF);
-    constexpr int gs = NT == 1 || L == 4 ? 4 / L : 2 / L < 1 ? 1 : 2 / L, rt = down_tiles(WF == kBf16, TMAX),
-                  ds = rt * NT >= 8 && L < 4 ? 2 / L : 4 / L;
+template <int WF, int NT>
+hipError_t launch_gate_up(const LayerArgs& p, hipStream_t s) {
+    // 16 (NT > 1: 8) loads of 16 bytes a lane and group
+    constexpr int L = loads_per_step(WF), KS = NT == 1 || L == 4 ? 4 / L : 2 / L < 1 ? 1 : 2 / L;
     const int64_t rows = p.T * p.k, experts = p.E < rows ? p.E : rows;
-    const size_t lds = plan_lds_bytes(p);
-    const int64_t units = experts * (p.F / 32);
-    const int64_t fit = 2 * device_cu_count();
-    auto gate_up = [&](auto full) {
-        hipLaunchKernelGGL((layer_gate_up_kernel<WF, NT, gs, decltype(full)::value>),
-                           dim3((unsigned)(units < fit ? units : fit)), dim3(64 * kGuWaves), lds, s, p);
-    };
-    if (p.H / 128 % gs == 0) gate_up(std::true_type{});
-    else gate_up(std::false_type{});
-    const hipError_t e = hipGetLastError();
+    const int64_t units = experts * (p.F / 32), fit = 2 * device_cu_count();
+    const dim3 grid((unsigned)(units < fit ? units : fit));
+    if (p.H / 128 % KS == 0)
+        hipLaunchKernelGGL((layer_gate_up_kernel<WF, NT, KS, true>), grid, dim3(64 * kGuWaves),
+                           plan_lds_bytes(p), s, p);
+    else
+        hipLaunchKernelGGL((layer_gate_up_kernel<WF, NT, KS, false>), grid, dim3(64 * kGuWaves),
+                           plan_lds_bytes(p), s, p);
+    return hipGetLastError();
+}
+
+template <int WF, int NT, int RT>
+hipError_t launch_down(const LayerArgs& p, hipStream_t s) {
+    // 4 loads a lane, tile and group, 2 where the rows' registers need the room
+    constexpr int L = loads_per_step(WF), KS = RT * NT >= 8 && L < 4 ? 2 / L : 4 / L;
+    const dim3 grid((unsigned)(p.H / (16 * RT) * p.split));
+    const size_t lds = down_lds(p.T, p.k, p.E, RT);
+    if (p.F / 128 % KS == 0)
+        hipLaunchKernelGGL((layer_down_kernel<WF, NT, KS, true, RT>), grid, dim3(64 * kDnWaves), lds, s, p);
+    else
+        hipLaunchKernelGGL((layer_down_kernel<WF, NT, KS, false, RT>), grid, dim3(64 * kDnWaves), lds, s, p);
+    return hipGetLastError();
+}
+
+// Tiles of 16 rows that a unit takes of an expert: enough for the rows that an
+// expert gets with evenly spread tokens and some more (mean + 3 sigma); an expert
+// with more rows takes further turns, its weights then coming from the L2.  One
+// tile leaves the registers to twice the weights in flight.
+int row_tiles(const LayerArgs& p) {
+    const int64_t mean = (p.T * p.k + p.E - 1) / p.E;
+    return p.T <= 16 || mean <= 8 ? 1 : p.T <= 32 || mean <= 18 ? 2 : 4;
+}
+
+template <int WF, int NT>
+hipError_t launch_layer_rows(const LayerArgs& p, hipStream_t s) {
+    hipError_t e = launch_gate_up<WF, NT>(p, s);
     if (e != hipSuccess) return e;
-    auto down = [&](auto full) {
-        hipLaunchKernelGGL((layer_down_kernel<WF, NT, ds, decltype(full)::value, rt, TMAX>),
-                           dim3((unsigned)(p.H / (16 * rt) * p.split)), dim3(64 * kDnWaves), lds, s, p);
-    };
-    if (p.F / 128 % ds == 0) down(std::true_type{});
-    else down(std::false_type{});
-    if (p.split > 1)
-        hipLaunchKernelGGL(layer_sum_kernel, dim3((unsigned)((p.T * p.H / 8 + 255) / 256)), dim3(256), 0, s, p);
+    const int rt = down_tiles(WF == kBf16, p.T, p.k, p.E);
+    e = rt == 1 ? launch_down<WF, NT, 1>(p, s) : rt == 2 ? launch_down<WF, NT, 2>(p, s)
+                                                         : launch_down<WF, NT, 4>(p, s);
+    if (e != hipSuccess || p.split == 1) return e;
+    hipLaunchKernelGGL(layer_sum_kernel, dim3((unsigned)((p.T * p.H / 8 + 255) / 256)), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
 template <int WF>
 hipError_t launch_layer_fmt(const LayerArgs& p, hipStream_t s) {
-    if (p.T <= 4) return launch_layer_rows<WF, 1, 4>(p, s);
-    if (p.T <= 16) return launch_layer_rows<WF, 1, 16>(p, s);
-    if (p.T <= 32) return launch_layer_rows<WF, 2, 32>(p, s);
-    return launch_layer_rows<WF, 4, kLayerMaxTokens>(p, s);
+    const int nt = row_tiles(p);
+    return nt == 1 ? launch_layer_rows<WF, 1>(p, s) : nt == 2 ? launch_layer_rows<WF, 2>(p, s)
+                                                              : launch_layer_rows<WF, 4>(p, s);
 }
 
 template <int XF, bool ODD>
@@ -685,14 +719,15 @@ hipError_t launch_linear4_few(bool x_fp4, const uint8_t* x, const uint8_t* xs, c
     return hipGetLastError();
 }
 
-int layer_split(bool bf16, int64_t T, int64_t H) {
-    const int64_t tiles = H / (16 * down_tiles(bf16, T)), s = (kSplitFull + tiles - 1) / tiles;
+int layer_split(bool bf16, int64_t T, int k, int E, int64_t H) {
+    const int64_t tiles = H / (16 * down_tiles(bf16, T, k, E)), s = (kSplitFull + tiles - 1) / tiles;
     return (int)(s < 8 ? s : 8);
 }
 
 hipError_t launch_layer(LayerWeights wf, const LayerArgs& p, hipStream_t s) {
     const unsigned grid = wf == LayerWeights::kBf16 ? 1u : 1u + (unsigned)p.T;
-    hipLaunchKernelGGL(layer_prep_kernel, dim3(grid), dim3(kPrepThreads), plan_lds(p.T, p.E), s, p);
+    hipLaunchKernelGGL(layer_prep_kernel, dim3(grid), dim3(kPrepThreads), prep_lds(p.T, p.E, p.k),
+                       s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     switch (wf) {

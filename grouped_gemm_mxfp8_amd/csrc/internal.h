@@ -217,7 +217,7 @@ struct LayerArgs {
     int split;               // workgroups that share columns of out (layer_split)
     float* parts;            // split > 1: [split][T][H] partial sums
 };
-int layer_split(bool bf16, int64_t T, int64_t H);
+int layer_split(bool bf16, int64_t T, int k, int E, int64_t H);
 hipError_t launch_layer(LayerWeights wf, const LayerArgs& p, hipStream_t s);
 
 int device_cu_count();

@@ -88,11 +88,25 @@ def test_against_the_oracle(dev, T, E, k, H, F, fmt):
     assert torch.equal(out, gm.moe_layer_fwd(x, logits, w1, w2, k))
 
 
-def test_1024_experts_64_slots(dev):
-    x, logits, w1, w2 = make(3, 1024, 128, 128, "mxfp4", 5, dev)
+@pytest.mark.parametrize("T,fmt", [(3, "mxfp4"), (40, "mxfp8"), (128, "bf16"), (128, "mxfp4")])
+def test_1024_experts_64_slots(dev, T, fmt):
+    """The largest plan (8192 rows at T = 128)."""
+    x, logits, w1, w2 = make(T, 1024, 128, 128, fmt, 5, dev)
     out = gm.moe_layer_fwd(x, logits, w1, w2, 64)
     torch.cuda.synchronize()
-    check(out, x, logits, w1, w2, 64, "mxfp4")
+    check(out, x, logits, w1, w2, 64, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,E,k", [(60, 64, 4), (100, 32, 2), (128, 128, 8)])
+def test_all_tokens_on_the_same_experts(dev, T, E, k, fmt):
+    """Far more rows on an expert than the even spread that the row tiles are
+    chosen for: its rows come in several turns."""
+    x, logits, w1, w2 = make(T, E, 256, 384, fmt, T + E, dev)
+    logits[:, 5:5 + k] += 50.0
+    out = gm.moe_layer_fwd(x, logits, w1, w2, k)
+    torch.cuda.synchronize()
+    check(out, x, logits, w1, w2, k, fmt)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
