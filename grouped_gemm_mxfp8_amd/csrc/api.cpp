@@ -479,16 +479,28 @@ static mx_status linear_mxfp4(bool x_fp4, const void* x, const uint8_t* x_scales
         return fail(MX_ERR_INVALID_ARG, "grouped_linear_fwd: MXFP4 needs x_scales and w_scales");
     if (K % 32 || N % 32)
         return fail(MX_ERR_UNSUPPORTED, "grouped_linear_fwd: MXFP4 needs K %% 32 == 0 and N %% 32 == 0");
-    if (K > kI32Max || N > kI32Max)
-        return fail(MX_ERR_UNSUPPORTED, "grouped_linear_fwd: operand too large");
+    // 16 rows of W in 32-bit bytes, 2^20 column blocks an expert in a 32-bit count
+    if (K > (1 << 26) || N > (1 << 26))
+        return fail(MX_ERR_UNSUPPORTED, "grouped_linear_fwd: MXFP4 needs K and N up to 2^26");
     if (!aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(y, 16))
         return fail(MX_ERR_INVALID_ARG,
                     "grouped_linear_fwd: y must be 16-byte aligned and scales 4-byte aligned");
     if (M == 0) return ok();
     const uint8_t *xc = static_cast<const uint8_t*>(x), *wc = static_cast<const uint8_t*>(w);
     const int64_t xld = x_fp4 ? K / 2 : K;
-    const bool tiles_fit = K % 128 == 0 && 256 * xld <= kI32Max && N <= (1 << 27);
-    if (tiles_fit && M > (int64_t)64 * E) {
+    // Tiles of 256 x 256 or the weight stream, by the average rows an expert gets:
+    // the stream's time grows with them, the tiles' hardly does, but few tiles
+    // leave most CUs idle for the length of K.  Rows where the two meet, measured
+    // at 1, 8 and 64 experts with K x N of 4096 x 4096, 2048 x 1408 and 1024 x 8192
+    // (MXFP4 x): 128 to 192 up to 64 tiles (one expert, 4096 x 4096: at 128 rows
+    // 29.0 us as a stream, 30.1 as tiles; at 192 rows 41.2 and 31.0), 64 to 96 up
+    // to two tiles a CU (8 experts, 4096 x 4096: at 64 rows 28.7 and 35.1, at 96
+    // 44.6 and 34.2), 8 to 48 beyond (64 experts, 1024 x 8192: at 32 rows 71.8 and
+    // 82.5, at 64 99.8 and 83.4).  MXFP8 x: the same, up to a third later.
+    const bool tiles_fit = K % 128 == 0 && 256 * xld <= kI32Max;
+    const int64_t tiles = E * ((N + 255) / 256);      // of up to 256 rows an expert
+    const int64_t stream_rows = tiles <= 64 ? 128 : tiles <= 512 ? 64 : 32;
+    if (tiles_fit && M > stream_rows * E) {
         mx::GemmProblem p{};
         p.offs = d_offsets;
         p.G = E;

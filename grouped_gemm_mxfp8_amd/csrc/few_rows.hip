@@ -2,7 +2,7 @@
 // layer for a few tokens (gfx950).  Both stream the weights once through the
 // core in few_rows.h.
 //
-// The layer runs as three launches on one stream:
+// The layer runs as three or four launches on one stream:
 //  * layer_prep: workgroup 0 routes (top-k by a bitwise search for the k-th
 //    largest key, softmax of the selected logits) and lists the routed rows
 //    sorted by (expert, token); the other workgroups quantize one token of x
@@ -698,7 +698,13 @@ void launch_few(const LinearArgs& a, int64_t M, hipStream_t s) {
         else
             hipLaunchKernelGGL((linear4_few_kernel<XF, NT, KS, false, ODD>), grid, dim3(256), 0, s, a);
     };
-    if (M <= 16) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
+    // One tile of rows leaves the registers to twice the weights in flight; past 16
+    // rows an expert's weights come again for every tile (from the L2).  Measured on
+    // 8 x (14336, 4096) with as many rows each, one / four tiles: 8 rows 42.7 / 48.7
+    // us, 16 47.4 / 52.5, 24 79.4 / 57.8; on 64 such experts 8 rows 360 / 414, 24 623
+    // / 495.  An average of 8 rows leaves few experts with more than 16.
+    if (M <= 16 || M <= (int64_t)8 * a.G)
+        go(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
     else go(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
 }
 

@@ -152,9 +152,10 @@ mx_status mxfp8_quantize(const void* x, int64_t batch, int64_t R, int64_t C,
  *                         [M][K/32]; w = codes [E][N][K/2] with w_scales
  *                         [E][N][K/32] (rowwise copies from mxfp4_quantize).
  *   dtype MX_DTYPE_MXFP8_MXFP4: x as for MXFP8, w as for MXFP4.
- *                         Both: K % 32 == 0, N % 32 == 0, K, N < 2^31; any M,
- *                         with the faster kernels where K % 128 == 0.  Nothing
- *                         is allocated.  A block with scale 255 makes the
+ *                         Both: K % 32 == 0, N % 32 == 0, K and N up to 2^26
+ *                         (MX_ERR_UNSUPPORTED otherwise); any M, with the
+ *                         faster kernels where K % 128 == 0.  Nothing is
+ *                         allocated.  A block with scale 255 makes the
  *                         outputs it takes part in NaN.
  *   d_row_scale  fp32 [M] routing weight applied to each output row, or NULL.
  *   y            bf16 [M][N].
@@ -492,8 +493,8 @@ mx_status moe_combine_bwd(const void* dout, int64_t T, int64_t H, int32_t k,
  * GroupedMLP's own operands), and for bf16 weights x as it is and z rounded to
  * bf16.  One call replaces moe_router, moe_route_plan, moe_permute_quantize,
  * the GroupedMLP forward and moe_combine, without quantizing weights; experts
- * that no token picks are not read.  Three launches, no host
- * synchronisation, one fixed order of every sum (two calls give the same bits).
+ * that no token picks are not read.  Three launches (four where few rows of
+ * output split the routed rows' sums), no host synchronisation, one fixed order of every sum (two calls give the same bits).
  *
  *   wdtype    MX_DTYPE_BF16: w1 bf16 [E][2F][H], w2 bf16 [E][H][F], scales NULL.
  *             MX_DTYPE_MXFP8, MX_DTYPE_MXFP4: rowwise copies of the same from

@@ -70,8 +70,10 @@ FP4, FP8FP4, BF16, FP8 = gm.MX_DTYPE_MXFP4, gm.MX_DTYPE_MXFP8_MXFP4, gm.MX_DTYPE
     (dict(ws=None), INVALID, "scales"),
     (dict(K=48), UNSUPPORTED, "K % 32"),
     (dict(N=40), UNSUPPORTED, "N % 32"),
-    (dict(N=1 << 32), UNSUPPORTED, "too large"),
-    (dict(K=1 << 32), UNSUPPORTED, "too large"),
+    (dict(N=1 << 32), UNSUPPORTED, "up to 2^26"),
+    (dict(K=1 << 32), UNSUPPORTED, "up to 2^26"),
+    (dict(N=(1 << 26) + 32), UNSUPPORTED, "up to 2^26"),
+    (dict(K=(1 << 26) + 32), UNSUPPORTED, "up to 2^26"),
     (dict(E=0), INVALID, "sizes"),
     (dict(E=1025), INVALID, "sizes"),
     (dict(M=-1), INVALID, "sizes"),

@@ -283,3 +283,66 @@ def test_more_tiles_than_workgroups(dev, K, fmt):
     x, w = values(xq), values(wq)
     assert_close(y, x, w, off, fmt=fmt)
     assert_close(ys, x, w, off, r, fmt=fmt)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("most,K,N", [
+    (8, 512, 160),          # one tile of rows a turn, for experts with more
+    (34, 256, 160),         # rows as a weight stream, up to several turns
+    (140, 256, 160),        # tiles of 256 x 256, one column of them
+    (34, 256, 2112),        # and nine
+])
+def test_many_uneven_experts(dev, most, K, N, fmt):
+    """64 experts with most rows on average, from none to ten times that."""
+    rng = np.random.default_rng(most + N)
+    counts = rng.multinomial(most * 64, rng.dirichlet(np.full(64, 0.4)))
+    xq, wq, off, offd, r = make(counts.tolist(), K, N, most, fmt, dev)
+    y = gm.grouped_linear_fwd(xq, offd, wq, row_scale=r)
+    torch.cuda.synchronize()
+    assert_close(y, values(xq), values(wq), off, r, fmt=fmt)
+
+
+def test_graph_replays_of_tiles(dev):
+    """Captured 256 x 256 tiles follow their offsets, empty experts among them."""
+    xq, wq, off, offd, r = make([400, 100, 300, 2], 512, 288, 21, "mxfp4", dev)
+    want0 = gm.grouped_linear_fwd(xq, offd, wq, row_scale=r)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = gm.grouped_linear_fwd(xq, offd, wq, row_scale=r)
+    for cut in ([400, 500, 800], [0, 0, 0], [802, 802, 802], [1, 257, 513], [400, 500, 800]):
+        offd[1:4] = torch.tensor(cut, device=dev)
+        graph.replay()
+        want = gm.grouped_linear_fwd(xq, offd, wq, row_scale=r)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+    assert torch.equal(y, want0)
+
+
+@pytest.mark.parametrize("fmt,M,N,K", [
+    ("mxfp4", 3, 32, 1 << 26), ("mxfp8", 17, 32, 1 << 26), ("mxfp4", 3, 32, (1 << 26) - 32),
+    ("mxfp4", 200, 64, (1 << 24) - 128), ("mxfp8", 200, 64, (1 << 23) - 128),
+])
+def test_longest_rows(dev, fmt, M, N, K):
+    """The largest K of either kernel: weights of zeros but for both ends of their rows."""
+    g = torch.Generator(device=dev).manual_seed(K % 97)
+    ends = [slice(0, 256), slice(K - 256, K)]
+    w = gm.Mx4Tensor(torch.zeros((1, N, K // 2), dtype=torch.uint8, device=dev),
+                     torch.full((1, N, K // 32), 127, dtype=torch.uint8, device=dev))
+    bits = 4 if fmt == "mxfp4" else 8
+    x = (gm.Mx4Tensor if fmt == "mxfp4" else gm.MxTensor)(
+        torch.full((M, K * bits // 8), 0x21, dtype=torch.uint8, device=dev),
+        torch.full((M, K // 32), 127, dtype=torch.uint8, device=dev))
+    small = lambda n: torch.randint(0, 112, n, generator=g, device=dev, dtype=torch.uint8)  # noqa: E731
+    xe, we = [], []
+    for e in ends:
+        at = slice(e.start // 2, e.stop // 2)
+        xat = at if fmt == "mxfp4" else e
+        w.codes[:, :, at] = small((1, N, 128))
+        x.codes[:, xat] = small((M, xat.stop - xat.start))
+        xe.append(values(type(x)(x.codes[:, xat].contiguous(), x.scales[:, :8].contiguous())))
+        we.append(values(gm.Mx4Tensor(w.codes[:, :, at].contiguous(), w.scales[:, :, :8].contiguous())))
+    off = np.array([0, M])
+    y = gm.grouped_linear_fwd(x, torch.from_numpy(off).to(dev), w)
+    torch.cuda.synchronize()
+    assert_close(y, np.concatenate(xe, 1), np.concatenate(we, 2), off, fmt=fmt)

@@ -260,3 +260,40 @@ def test_weights_past_4_gib(dev):
     want = gm.moe_layer_fwd(x, torch.zeros((T, 1), device=dev), a, b, 1)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and out.any()
+
+
+def test_mxfp4_operators_together(dev):
+    """A serving program's two ways through an MXFP4 layer, from one quantization
+    of the weights: the grouped products over a prompt's rows, stage by stage,
+    and the layer call for a step's tokens.
+
+    Tolerance of the last comparison.  The grouped way rounds h to bf16 (twice
+    2^-8 / (2 sqrt 3) in RMS: 1.6e-3 of a and of b) and z to bf16 (1.1e-3) before
+    it quantizes z: z moves by about d = 2.5e-3 of itself.  A value that moves
+    by d crosses an E4M3 step of s = 2^-4 .. 2^-3 of itself with probability d / s
+    and then moves by s: sqrt(d s) = 1.3e-2 to 1.8e-2 in RMS.  y's own rounding
+    adds 1e-3.  Twice the middle of that: 3e-2."""
+    T, E, k, H, F = 96, 8, 2, 512, 640
+    x, logits, w1, w2 = make(T, E, H, F, "bf16", 40, dev)
+    q1, q2 = gm.mxfp4_quantize(w1)["row"], gm.mxfp4_quantize(w2)["row"]
+    ids, w = gm.router(logits, k)
+    off, row_of, tok_of, r = gm.route_plan(ids, E, w)
+    xq = gm.permute_quantize(x, tok_of, off, T * k, colwise=False)["row"]
+    h = gm.grouped_linear_fwd(xq, off, q1)
+    a, b = h[:, :F].float(), h[:, F:].float()
+    z = gm.mxfp8_quantize((r[:, None] * torch.nn.functional.silu(a) * b).bfloat16())["row"]
+    y = gm.grouped_linear_fwd(z, off, q2)
+    got = gm.combine(y, row_of)
+    torch.cuda.synchronize()
+    # the products, against their operands' values (2^-8 and the E4M3 term 2^-10 S)
+    offs = off.cpu().numpy()
+    for p, u, v in ((h, values(xq), values(q1)), (y, values(z), values(q2))):
+        ref, S = O.grouped_linear(u, v, offs), O.grouped_linear(np.abs(u), np.abs(v), offs)
+        assert (np.abs(to64(p) - ref) <= 2.0 ** -8 * np.abs(ref) + 1.01 * 2.0 ** -10 * S).all()
+    # the weights the layer reads are the ones that dequantize to these values
+    assert np.array_equal(to64(gm.mxfp4_dequantize(q1)), values(q1))
+    out = gm.moe_layer_fwd(x, logits, q1, q2, k)
+    torch.cuda.synchronize()
+    check(out, x, logits, q1, q2, k, "mxfp4")
+    rel, _ = O.parity_metrics(to64(got), to64(out))
+    assert rel <= 3e-2, rel
