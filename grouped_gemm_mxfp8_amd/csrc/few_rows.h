@@ -105,9 +105,11 @@ struct Tile {
             const int st = ODD || !FULL ? min(step + i, last - 1) : step + i;
 #pragma unroll
             for (int l = 0; l < kL; ++l) {
-                // ODD: a chunk past K reads the row's first one instead
+                // ODD: a chunk past K reads the row's first 16 bytes instead (the
+                // lane's 16 q taken back: a row may have no more than those)
                 const bool in = !ODD || value(st, l, q) < K;
-                c[i * kL + l] = src.codes16(in ? (uint32_t)(st * bytes_per_step(F)) : 0u, in ? l * 64 : 0);
+                c[i * kL + l] =
+                    src.codes16(in ? (uint32_t)(st * bytes_per_step(F)) : 0u, in ? l * 64 : -16 * q);
             }
         }
         if constexpr (F == kBf16) {

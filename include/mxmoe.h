@@ -220,7 +220,8 @@ mx_status grouped_linear_fwd_fp8(const uint8_t* x, const float* d_x_scale_inv,
  *   col_codes   uint8 [batch][C][R/2] and col_scales [batch][C][R/32]: the
  *               transposed copy, blocks along R, R % 32 == 0 (for weights
  *               [E][N][K]: the operand of the data gradient, see
- *               grouped_linear_fwd).  Both NULL to skip.  batch <= 65535.
+ *               grouped_linear_fwd).  Both NULL to skip.  batch <= 65535,
+ *               C <= 4194240 (64 * 65535).
  *   At least one copy.  x and codes 16-byte aligned.  x must not overlap an
  *   output.
  * mxfp4_dequantize -- bf16 y [rows][C] of codes [rows][C/2] and scales
