@@ -27,6 +27,15 @@ namespace {
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 
+// x is read once: loads that do not keep its lines in the caches leave those to
+// the codes.  64 x (2048 x 1408) by columns 116 -> 96 us (4.9 TB/s), 16384 x 4096 by
+// rows 32 -> 26.5 us (6.4 TB/s), inputs changing from call to call.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+
 // elementwise max of two pairs of 16-bit magnitudes
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     const u16x2 r = __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b));
@@ -64,7 +73,7 @@ quant4_rows_kernel(const uint4* __restrict__ x, int64_t units, uint32_t* __restr
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const int64_t u = u0 + i * 256;
-        if (u < units) v[i] = x[u];
+        if (u < units) v[i] = load_once(x + u);
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
@@ -104,7 +113,7 @@ quant4_cols_kernel(const uint16_t* __restrict__ x, int64_t R, int64_t C, uint8_t
         const int row = i * 32 + (tid >> 3);
         uint4 v = make_uint4(0, 0, 0, 0);
         if (r0 + row < R && c0 + lc < C)
-            v = *reinterpret_cast<const uint4*>(xb + (r0 + row) * C + c0 + lc);
+            v = load_once(xb + (r0 + row) * C + c0 + lc);
         *reinterpret_cast<uint4*>(&tile[row * 32 + i * 8 + lc / 2]) = v;
     }
     __syncthreads();
