@@ -511,7 +511,10 @@ layer_gate_up_kernel(LayerArgs p) {
 // ---- the layer: down and combine -------------------------------------------------
 
 constexpr int kDnWaves = 8;
-constexpr int kSplitFull = 256;    // workgroups of the down projection, one a CU
+// Workgroups of the down projection: one a CU.  64 tokens on 64 x (2048, 1408) MXFP4,
+// 128 / 256 / 384 / 512 workgroups: 43 / 28 / 46 / 38 us (a workgroup's eight waves
+// take a CU's registers, so more of them run one after the other).
+constexpr int kSplitFull = 256;
 
 // LDS of a down-projection workgroup: the plan, and its waves' sums of T tokens
 // by 16 rt columns.
