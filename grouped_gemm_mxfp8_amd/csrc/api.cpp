@@ -680,7 +680,10 @@ constexpr uint32_t kFwdFlags = MX_FWD_REUSE_WEIGHTS | MX_MLP_SAVE_H;
 
 // ---- MXFP4 ---------------------------------------------------------------------
 namespace {
-constexpr int64_t kMx4MaxValues = (int64_t)1 << 44;   // flat launches of 8192 values a workgroup
+// Flat launches: 8192 values a workgroup of 256 threads, and a launch holds fewer
+// than 2^32 threads.  (By columns a workgroup has 256 rows: with C >= 32 fewer
+// than 2^32 rows, which is as many workgroups along x.)
+constexpr int64_t kMx4MaxValues = (((int64_t)1 << 24) - 1) * 8192;
 
 // a * b <= limit for non-negative a, b, without overflow
 bool product_within(int64_t a, int64_t b, int64_t limit) { return a == 0 || b <= limit / a; }

@@ -227,7 +227,8 @@ mx_status grouped_linear_fwd_fp8(const uint8_t* x, const float* d_x_scale_inv,
  * mxfp4_dequantize -- bf16 y [rows][C] of codes [rows][C/2] and scales
  *   [rows][C/32], C % 32 == 0; every value is exact, a block with scale 255
  *   gives NaN.  codes and y 16-byte aligned.
- * rows * C below 2^44 in both.
+ * Both take up to 2^37 - 8192 values (MX_ERR_UNSUPPORTED above: a launch holds
+ * no more).
  */
 mx_status mxfp4_quantize(const void* x, int64_t batch, int64_t R, int64_t C, uint8_t* row_codes,
                          uint8_t* row_scales, uint8_t* col_codes, uint8_t* col_scales,

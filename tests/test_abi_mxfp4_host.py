@@ -137,3 +137,18 @@ def test_layer_workspace_bytes(mxlib):
     assert f(FP4, 129, E, k, H, F) == 0 and f(FP8FP4, T, E, k, H, F) == 0
     # the largest sizes do not overflow
     assert f(BF16, 128, 1024, 64, 1 << 24, 1 << 24) > 128 * 64 * (1 << 25)
+
+
+@pytest.mark.parametrize("batch,R,C", [
+    (1, 1 << 32, 32), (1, 1 << 20, 1 << 17), (1 << 15, 1 << 17, 32),
+    (1, (1 << 32) - 128, 32),              # 2^37 - 4096: one workgroup more than fit
+    (1, 1 << 38, 32), (3, 1 << 30, 1 << 10),
+])
+def test_sizes_past_what_a_launch_takes_are_refused(mxlib, batch, R, C):
+    """A launch holds fewer than 2^32 threads, which take 32 values each, 256 of
+    them a workgroup: larger tensors are refused, not left to the launch."""
+    for args in ((P, P, None, None), (None, None, P, P), (P, P, P, P)):
+        assert mxlib.mxfp4_quantize(P, batch, R, C, *args, None) == UNSUPPORTED
+        assert "too large" in err(mxlib)
+    assert mxlib.mxfp4_dequantize(P, P, batch * R, C, P, None) == UNSUPPORTED
+    assert "too large" in err(mxlib)
