@@ -639,12 +639,14 @@ hipError_t launch_gate_up(const LayerArgs& p, hipStream_t s) {
     const int64_t rows = p.T * p.k, experts = p.E < rows ? p.E : rows;
     const int64_t units = experts * (p.F / 32), fit = 2 * device_cu_count();
     const dim3 grid((unsigned)(units < fit ? units : fit));
-    if (p.H / 128 % KS == 0)
-        hipLaunchKernelGGL((layer_gate_up_kernel<WF, NT, KS, true>), grid, dim3(64 * kGuWaves),
-                           plan_lds_bytes(p), s, p);
-    else
-        hipLaunchKernelGGL((layer_gate_up_kernel<WF, NT, KS, false>), grid, dim3(64 * kGuWaves),
-                           plan_lds_bytes(p), s, p);
+    if constexpr (KS > 1)               // (groups of one step are always whole)
+        if (p.H / 128 % KS) {
+            hipLaunchKernelGGL((layer_gate_up_kernel<WF, NT, KS, false>), grid, dim3(64 * kGuWaves),
+                               plan_lds_bytes(p), s, p);
+            return hipGetLastError();
+        }
+    hipLaunchKernelGGL((layer_gate_up_kernel<WF, NT, KS, true>), grid, dim3(64 * kGuWaves),
+                       plan_lds_bytes(p), s, p);
     return hipGetLastError();
 }
 
@@ -654,10 +656,12 @@ hipError_t launch_down(const LayerArgs& p, hipStream_t s) {
     constexpr int L = loads_per_step(WF), KS = RT * NT >= 8 && L < 4 ? 2 / L : 4 / L;
     const dim3 grid((unsigned)(p.H / (16 * RT) * p.split));
     const size_t lds = down_lds(p.T, p.k, p.E, RT);
-    if (p.F / 128 % KS == 0)
-        hipLaunchKernelGGL((layer_down_kernel<WF, NT, KS, true, RT>), grid, dim3(64 * kDnWaves), lds, s, p);
-    else
-        hipLaunchKernelGGL((layer_down_kernel<WF, NT, KS, false, RT>), grid, dim3(64 * kDnWaves), lds, s, p);
+    if constexpr (KS > 1)
+        if (p.F / 128 % KS) {
+            hipLaunchKernelGGL((layer_down_kernel<WF, NT, KS, false, RT>), grid, dim3(64 * kDnWaves), lds, s, p);
+            return hipGetLastError();
+        }
+    hipLaunchKernelGGL((layer_down_kernel<WF, NT, KS, true, RT>), grid, dim3(64 * kDnWaves), lds, s, p);
     return hipGetLastError();
 }
 
@@ -675,8 +679,10 @@ hipError_t launch_layer_rows(const LayerArgs& p, hipStream_t s) {
     hipError_t e = launch_gate_up<WF, NT>(p, s);
     if (e != hipSuccess) return e;
     const int rt = down_tiles(WF == kBf16, p.T, p.k, p.E);
-    e = rt == 1 ? launch_down<WF, NT, 1>(p, s) : rt == 2 ? launch_down<WF, NT, 2>(p, s)
-                                                         : launch_down<WF, NT, 4>(p, s);
+    if (rt == 1) e = launch_down<WF, NT, 1>(p, s);
+    else if (rt == 2) e = launch_down<WF, NT, 2>(p, s);
+    else if constexpr (WF != kBf16 && NT < 4) e = launch_down<WF, NT, 4>(p, s);
+    else e = hipErrorInvalidValue;      // (four tiles: MX weights, at most 32 tokens, so NT <= 2)
     if (e != hipSuccess || p.split == 1) return e;
     hipLaunchKernelGGL(layer_sum_kernel, dim3((unsigned)((p.T * p.H / 8 + 255) / 256)), dim3(256), 0, s, p);
     return hipGetLastError();
