@@ -98,6 +98,19 @@ def test_1024_experts_64_slots(dev, T, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("F", [384, 512])
+@pytest.mark.parametrize("E", [64, 512])
+def test_large_plans_with_many_rows_an_expert(dev, E, F, fmt):
+    """128 tokens, 64 slots: the plan leaves the LDS of a down workgroup to one
+    tile of W2, with two (512 experts) or four (64) tiles of rows; F of whole
+    and of partial groups of steps."""
+    x, logits, w1, w2 = make(128, E, 128, F, fmt, E + F, dev)
+    out = gm.moe_layer_fwd(x, logits, w1, w2, 64)
+    torch.cuda.synchronize()
+    check(out, x, logits, w1, w2, 64, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("T,E,k", [(60, 64, 4), (100, 32, 2), (128, 128, 8)])
 def test_all_tokens_on_the_same_experts(dev, T, E, k, fmt):
     """Far more rows on an expert than the even spread that the row tiles are
