@@ -136,6 +136,31 @@ def test_products_of_a_run_of_eight_are_aligned(dev):
         assert dot(40, big * 2.0 ** -d) == big * 2.0 ** -d, d
 
 
+def test_the_alignment_drops_what_lies_below(dev):
+    """The other side of that fact: within the run of eight, a product is cut
+    toward zero to a multiple of 2^-13 of the large ones; the next run is not
+    touched."""
+    e4 = lambda t: t.to(torch.float8_e4m3fn).view(torch.uint8).to(dev)  # noqa: E731
+    one = lambda *s: torch.full(s, 127, dtype=torch.uint8, device=dev)  # noqa: E731
+    w = torch.zeros(1, 32, 128)
+    w[:, :, :2], w[:, :, 2:16] = 4.0, 1.0
+    wq = gm.mxfp4_quantize(w.bfloat16().to(dev))["row"]
+    grid = 256.0 * 4.0 * 2.0 ** -13
+    # (place among the K values, value, what is left of it); E4M3 ends at 2^-9
+    cases = [(at, sign * p, sign * (p // grid * grid if at < 8 else p))
+             for at in (2, 7, 8, 15) for sign in (1.0, -1.0)
+             for p in (1.75, 0.9375, 0.1875, 0.125, 0.1171875, 0.0625, 0.015625, 2.0 ** -9)]
+    x = torch.zeros(len(cases), 128)
+    x[:, 0], x[:, 1] = 256.0, -256.0
+    for i, (at, p, _) in enumerate(cases):
+        x[i, at] = p
+    off = torch.tensor([0, len(cases)], device=dev)
+    y = gm.grouped_linear_fwd(gm.MxTensor(e4(x), one(len(cases), 4)), off, wq)
+    torch.cuda.synchronize()
+    assert y[:, 0].tolist() == [left for _, _, left in cases]
+    assert torch.equal(y, y[:, :1].expand_as(y))
+
+
 @pytest.mark.parametrize("M", [5, 400])
 def test_nan_blocks_stay_in_their_row_and_column(dev, M):
     xq, wq, off, offd, _ = make([M, 3], 512, 160, 4, "mxfp4", dev)
