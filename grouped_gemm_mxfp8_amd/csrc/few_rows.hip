@@ -10,9 +10,11 @@
 //  * layer_gate_up: a workgroup takes 32 columns of F of one routed expert (64
 //    rows of W1), its four waves a quarter of H each; z = r silu(a) b leaves
 //    as MXFP8 blocks (MX weights) or bf16.
-//  * layer_down: a workgroup takes 16 rows of every routed expert's W2 and adds
-//    the experts' products in fp32 in LDS, so the combine needs no atomics, no
-//    second pass and has one fixed order.
+//  * layer_down: a workgroup takes 16, 32 or 64 rows of every routed expert's
+//    W2, or a share of their products where few such rows would leave CUs idle,
+//    and adds the experts' products in fp32 in LDS: the combine needs no atomics
+//    and has one fixed order.
+//  * layer_sum: adds those shares, where there are any.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -42,7 +44,12 @@ struct LinearArgs {
 
 // A workgroup's units: 64 columns of y for up to 16 NT rows of one expert, the
 // four waves a quarter of K each.  Units run over (expert with rows, column
-// block), and over an expert's row chunks within one.
+// block), and over an expert's row chunks within one: rows that an expert has
+// beyond a chunk lengthen its workgroups' turn instead of filling other CUs.
+// Made for few rows, where the weights' one reading is the time (16 rows on 8 x
+// (28672, 4096): 78 us, 5.6 TB/s); 16384 rows of K = 2880 on one expert of 4096
+// columns (64 workgroups, 256 turns) take 2.2 ms, as 256 x 256 tiles of K = 2944
+// 0.12.
 template <int XF, int NT, int kSteps, bool FULL, bool ODD>
 __global__ void __launch_bounds__(64 * kLinWaves, 2)
 linear4_few_kernel(LinearArgs p) {
@@ -482,6 +489,9 @@ layer_gate_up_kernel(LayerArgs p) {
                         up[0] += b.x;
                         up[1] += b.y;
                     }
+                // (the hardware's exp and reciprocal, as in the GroupedMLP's epilogue:
+                // silu is off by at most some (|g| + 4) 2^-23 of itself, 1e-6 for
+                // usual g, against the 2^-4 (bf16: 2^-8) of z's own rounding)
                 float z[2];
 #pragma unroll
                 for (int v = 0; v < 2; ++v)
@@ -529,7 +539,10 @@ constexpr size_t kLdsBytes = 160 * 1024;
 // W2.  One tile: H / 16 workgroups fill the CUs and no sums of parts are left to
 // add.  Measured on 8 x (4096, 14336) MXFP4, all experts, one / two / four tiles:
 // T = 4 60 / - / - us, T = 16 92 / 68 / 67, T = 32 - / 94 / 78; 64 tokens on 64 x
-// (2048, 1408) 35 / 28 / -; bf16, 16 tokens: 155 / 156 / 170.
+// (2048, 1408) 35 / 28 / -; bf16, 16 tokens: 155 / 156 / 170.  Past 32 tokens the
+// whole layer with two / four tiles: on 8 x (4096, 14336), top 2, MXFP4 33 tokens
+// 177 / 180 us, 64 213 / 210, MXFP8 305 / 318 and 342 / 351; on 64 x (2048, 1408),
+// top 8, MXFP4 79 / 76 and 81 / 85, MXFP8 115 / 115 and 123 / 122.
 int down_tiles(bool bf16, int64_t T, int k, int E) {
     int rt = T <= 4 || (bf16 && T <= 16) ? 1 : T <= 16 || T > 32 || bf16 ? 2 : 4;
     while (rt > 1 && down_lds(T, k, E, rt) > kLdsBytes) rt /= 2;
@@ -538,7 +551,7 @@ int down_tiles(bool bf16, int64_t T, int k, int E) {
 
 // `split` workgroups share rows h0 .. h0 + 16 RT - 1 of every routed expert's W2.  Their
 // waves' units are (expert, part of F, chunk of rows); each wave adds its units'
-// products to its own sums[token][16], and the waves' sums are added in order.
+// products to its own sums[token][16 RT], and the waves' sums are added in order.
 // With split > 1 a workgroup leaves its sums in `parts` and layer_sum adds them.
 // (Adding them in the last workgroup to arrive took six times as long: the
 // fences that such a hand-over needs write the XCD's L2 back, 0.3 us each.)
