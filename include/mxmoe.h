@@ -235,7 +235,8 @@ mx_status grouped_linear_fwd_fp8(const uint8_t* x, const float* d_x_scale_inv,
  *   output.
  * mxfp4_dequantize -- bf16 y [rows][C] of codes [rows][C/2] and scales
  *   [rows][C/32], C % 32 == 0; every value is exact, a block with scale 255
- *   gives NaN.  codes and y 16-byte aligned.
+ *   gives NaN, and values past the largest bf16 (scales 253 and 254, which
+ *   mxfp4_quantize never gives) infinities.  codes and y 16-byte aligned.
  * Both take up to 2^37 - 8192 values (MX_ERR_UNSUPPORTED above: a launch holds
  * no more).
  */

@@ -311,6 +311,22 @@ def test_more_tiles_than_workgroups(dev, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("counts,K,N", [
+    ([9000], 2080, 32),             # one expert, one column block, 141 turns
+    ([700, 0, 1300, 1], 1056, 160),
+    ([65, 4000, 3], 4064, 96),
+    ([2048] + [0] * 63, 512, 8192),     # whole K: an average of 32 rows, all on one expert
+    ([1, 0, 1985] + [1] * 30, 160, 544),
+])
+def test_many_turns_of_an_expert(dev, counts, K, N, fmt):
+    """Experts whose rows take many turns of the weight stream."""
+    xq, wq, off, offd, r = make(counts, K, N, K + N, fmt, dev)
+    y = gm.grouped_linear_fwd(xq, offd, wq, row_scale=r)
+    torch.cuda.synchronize()
+    assert_close(y, values(xq), values(wq), off, r, fmt=fmt)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("most,K,N", [
     (8, 512, 160),          # one tile of rows a turn, for experts with more
     (34, 256, 160),         # rows as a weight stream, up to several turns

@@ -98,6 +98,19 @@ def test_1024_experts_64_slots(dev, T, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,E,k,H,F", [
+    (1, 2, 1, 4096, 14336),
+    (20, 3, 2, 7168, 2048),
+    (48, 5, 2, 2816, 1920),
+])
+def test_real_sizes_against_the_oracle(dev, T, E, k, H, F, fmt):
+    x, logits, w1, w2 = make(T, E, H, F, fmt, H + F, dev)
+    out = gm.moe_layer_fwd(x, logits, w1, w2, k)
+    torch.cuda.synchronize()
+    check(out, x, logits, w1, w2, k, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("F", [384, 512])
 @pytest.mark.parametrize("E", [64, 512])
 def test_large_plans_with_many_rows_an_expert(dev, E, F, fmt):
