@@ -27,9 +27,16 @@
 // Precision.  The sums are fp32, but with an E4M3 operand that MFMA first cuts
 // the eight products of each run of eight K values to multiples of 2^-13 of
 // their largest (E2M1 x E2M1 products span less than that and lose nothing).
-// At K = 2048 a model of that rule puts a sum off by 2e-5 (E2M1 weights) to 6e-5
-// (E4M3) of itself in RMS.  It is what every MXFP8 product of the library has; an exact sum would
-// take the bf16 MFMA, with the operands converted in registers at half its rate.
+// The GroupedLinear takes that, as every MXFP8 product of the library: its bf16
+// result is coarser by far, except where large products cancel.  The layer does
+// not: z is quantized from its first sums, and at K = 2048 the cut put those off
+// by 2e-5 to 6e-5 of themselves, which moved large values of z by whole E4M3
+// steps (out off by up to 3.0e-3 in norm, the rounding of out alone 1.7e-3).
+// Its products are exact: operands converted to bf16 in registers, on the bf16
+// MFMA (out off by 1.7e-3, bit for bit an fp32 sum's in most cases).  The
+// conversions cost 1 to 2 % of the layer's time with MXFP8 weights and 2 to 8 %
+// with MXFP4 (1 token, 8 x (4096, 14336): 48.4 -> 51.6 us; 64 tokens 208 -> 211;
+// 64 x (2048, 1408), 16 tokens: 73.1 -> 78.3).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -81,6 +88,51 @@ __device__ __forceinline__ v4f mac_step(v4f acc, const u32x4* w, uint32_t ws, co
             mx_frag<WF>(w), mx_frag<XF>(x), acc, WF == kFp4 ? 4 : 0, XF == kFp4 ? 4 : 0, 0, (int)ws, 0,
             (int)xs);
     }
+}
+
+// Exact products of MX operands: the values that codes and scales stand for, as
+// bf16 (at most 4 significant bits; exact from 2^-126 up, and past bf16's largest,
+// which no quantizer's blocks reach, infinity), on the bf16 MFMA, whose products
+// and sums are fp32.  Its 32 values of K are four times eight, lane (r, q) holding
+// eight of row r: any eight, as long as both operands hold the same.
+
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+
+// The scale of byte b of s, an E8M0 code, as the conversions take it: its bits as
+// an fp32 exponent.  (They read exponent 0 as 2^-127 and 255 as NaN, whatever the
+// code: checked on the device for every code and scale.)
+__device__ __forceinline__ float block_scale(uint32_t s, int b) {
+    return __uint_as_float(__builtin_amdgcn_ubfe(s, 8 * b, 8) << 23);
+}
+
+// Eight values of a lane's chunk j (of four) of a step as bf16.  c: the step's
+// codes, s: the scale of the chunk's block.  MXFP4: dword j of the lane's 32
+// values.  MXFP8: dwords 2 j and 2 j + 1.
+template <int F>
+__device__ __forceinline__ bf16x8 exact_chunk(const u32x4* c, float s, int j) {
+    uint32_t v[4];
+    auto put = [&](int i, const bf16x2v& p) { v[i] = __builtin_bit_cast(uint32_t, p); };
+    if constexpr (F == kFp4) {
+        const uint32_t d = c[0][j];
+        put(0, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 0));
+        put(1, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 1));
+        put(2, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 2));
+        put(3, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 3));
+    } else {
+        const int a = (int)c[j >> 1][2 * (j & 1)], b = (int)c[j >> 1][2 * (j & 1) + 1];
+        put(0, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, false));
+        put(1, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, true));
+        put(2, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, false));
+        put(3, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, true));
+    }
+    return __builtin_bit_cast(bf16x8, u32x4{v[0], v[1], v[2], v[3]});
+}
+// The scale of chunk j, s: the step's four.  Where both operands are MXFP8 a lane
+// holds K values 16 q .. and 64 + 16 q .., of blocks q / 2 and 2 + q / 2; MXFP4
+// weights and rows beside them (RUN) 32 q .., of block q.
+template <bool RUN>
+__device__ __forceinline__ float exact_scale(uint32_t s, int j, int q) {
+    return RUN ? block_scale(s, q) : block_scale(s, 2 * (j >> 1) + (q >> 1));
 }
 
 // kSteps consecutive 128-value steps of one 16-row tile in registers.
@@ -221,11 +273,22 @@ struct XRow {
     }
     __device__ __forceinline__ uint32_t scale1(uint32_t at) const { return scales[at]; }
 };
+// The same with 32 values in a row: a lane's two loads of a step are at 32 q and
+// 32 q + 16 (MXFP8 rows beside MXFP4 weights, exact products).
+struct XRowRun : XRow {
+    __device__ __forceinline__ u32x4 codes16(uint32_t at, int imm) const {
+        return XRow::codes16(at, imm / 4);
+    }
+};
 template <int F>
 __device__ __forceinline__ XRow x_row(const uint8_t* codes, const uint8_t* scales, int64_t row, int64_t K,
                                       int lane) {
     return XRow{codes + row * row_bytes(F, K) + (lane >> 4) * 16,
                 F == kBf16 ? nullptr : scales + row * (K / 32)};
+}
+__device__ __forceinline__ XRowRun x_row_run(const uint8_t* codes, const uint8_t* scales, int64_t row, int64_t K,
+                                             int lane) {
+    return XRowRun{{codes + row * K + (lane >> 4) * 32, scales + row * (K / 32)}};
 }
 
 // One unit of a wave's work, all of it wave-uniform: RT tiles of weights (their
@@ -260,7 +323,8 @@ __device__ __forceinline__ void share(int steps, int wave, int waves, int& s0, i
 // too (from the L2), for as many of their tiles as the registers hold, skipping
 // tiles without rows.  (Issued after them, the rows waited for the next weights
 // and the stream lost its overlap.)
-template <int WF, int XF, int RT, int NT, int kSteps, bool FULL, bool ODD, class First, class Next,
+// EXACT: exact products of MX operands (XF MXFP8; MXFP4 weights: rows by x_row_run).
+template <int WF, int XF, int RT, int NT, int kSteps, bool FULL, bool ODD, bool EXACT, class First, class Next,
           class XRowOf, class Ending, class Done>
 __device__ __forceinline__ void stream(int64_t K, int lane, First first, Next next, XRowOf xrow,
                                        Ending ending, Done done) {
@@ -326,6 +390,37 @@ __device__ __forceinline__ void stream(int64_t K, int lane, First first, Next ne
     constexpr std::integral_constant<int, 0> k0{};
     constexpr std::integral_constant<int, kFirst> kF{};
     constexpr std::integral_constant<int, NT> kN{};
+    // mac for all tiles of rows, with exact products: each chunk of rows is converted
+    // once for TG tiles of weights, each chunk of weights once, and only one
+    // chunk's values live at a time.  (TG: half of the tiles where the registers
+    // are full, the compiler would spill rows.)
+    auto mac_exact = [&](const Group& g, const TX* x, const U& u, int step) {
+        constexpr bool kRun = WF == kFp4;
+        constexpr int TG = RT == 4 && NT == 4 && kSteps > 1 ? 2 : RT;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+            if (FULL || i == 0 || step + i < u.s1) {
+#pragma unroll
+                for (int h = 0; h < 4 * (RT / TG); ++h) {
+                    const int j = h / (RT / TG), t0 = h % (RT / TG) * TG;
+                    __builtin_amdgcn_sched_barrier(0);
+                    bf16x8 w[TG];
+#pragma unroll
+                    for (int t = 0; t < TG; ++t)
+                        w[t] = exact_chunk<WF>(g.w[t0 + t].c + i * TW::kL,
+                                                           exact_scale<kRun>(g.w[t0 + t].s[i], j, q), j);
+                    tiles(k0, kN, u, [&](auto nc) {
+                        constexpr int n = decltype(nc)::value;
+                        const bf16x8 xv = exact_chunk<XF>(
+                            x[n].c + i * TX::kL, exact_scale<kRun>(x[n].s[i], j, q), j);
+#pragma unroll
+                        for (int t = 0; t < TG; ++t)
+                            acc[t0 + t][n] =
+                                __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[t], xv, acc[t0 + t][n], 0, 0, 0);
+                    });
+                }
+            }
+    };
     U u;
     if (!first(u)) return;
     int step = u.s0;
@@ -352,12 +447,17 @@ __device__ __forceinline__ void stream(int64_t K, int lane, First first, Next ne
         load(other, v, vstep, more);
         __builtin_amdgcn_sched_barrier(0);
         if (live) {
-            tiles(k0, kF, u, [&](auto nc) { mac(mine, xs[decltype(nc)::value], nc, u, step); });
-            tiles(kF, kN, u, [&](auto nc) {
-                TX x;
-                load_x(x, u, decltype(nc)::value, step);
-                mac(mine, x, nc, u, step);
-            });
+            if constexpr (EXACT) {
+                static_assert(!EXACT || (kFirst == NT && XF == kFp8 && WF != kBf16 && !ODD), "all tiles in registers");
+                mac_exact(mine, xs, u, step);
+            } else {
+                tiles(k0, kF, u, [&](auto nc) { mac(mine, xs[decltype(nc)::value], nc, u, step); });
+                tiles(kF, kN, u, [&](auto nc) {
+                    TX x;
+                    load_x(x, u, decltype(nc)::value, step);
+                    mac(mine, x, nc, u, step);
+                });
+            }
             if (step + kSteps >= u.s1) {
                 done(acc, u);
                 clear();

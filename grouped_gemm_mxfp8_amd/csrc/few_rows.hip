@@ -15,6 +15,7 @@
 //    and adds the experts' products in fp32 in LDS: the combine needs no atomics
 //    and has one fixed order.
 //  * layer_sum: adds those shares, where there are any.
+// Sums are fp32 of exact products in all formats.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -109,7 +110,7 @@ linear4_few_kernel(LinearArgs p) {
     };
     int turn = 0;
     float scale[NT];                 // row scale of this thread's token in done
-    stream<kFp4, XF, 4, NT, kSteps, FULL, ODD>(
+    stream<kFp4, XF, 4, NT, kSteps, FULL, ODD, false>(
         p.K, lane, [&](U& u) { return place(u, blockIdx.x, -1); },
         [&](U& u) {
             const int64_t hi = uni64(s_hi[u.id / ncol]);
@@ -336,8 +337,8 @@ size_t prep_lds(int64_t T, int E, int k) {
 }
 
 // MXFP8 blocks of one token (H % 128 == 0), as mxfp8_quantize makes them; a
-// block with an infinity or a NaN gets the NaN scale, so that the token's
-// output says so.
+// block with an infinity or a NaN becomes NaNs, so that the token's output says
+// so.
 __device__ void quant_token(const uint16_t* __restrict__ x, int H, uint8_t* __restrict__ codes,
                             uint8_t* __restrict__ scales) {
     for (int u = threadIdx.x; u < H / 8; u += kPrepThreads) {
@@ -358,9 +359,9 @@ __device__ void quant_token(const uint16_t* __restrict__ x, int H, uint8_t* __re
         const float lim = e4m3_limit_from_code(c), s = scale_from_code(c);
         uint2 o = make_uint2(e4m3x4_scaled(v[0], v[1], v[2], v[3], lim, s),
                              e4m3x4_scaled(v[4], v[5], v[6], v[7], lim, s));
-        if (bad) o = make_uint2(0u, 0u);
+        if (bad) o = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
         *reinterpret_cast<uint2*>(codes + u * 8) = o;
-        if ((threadIdx.x & 3) == 0) scales[u >> 2] = bad ? 255 : (uint8_t)c;
+        if ((threadIdx.x & 3) == 0) scales[u >> 2] = bad ? 127 : (uint8_t)c;
     }
 }
 
@@ -445,7 +446,7 @@ layer_gate_up_kernel(LayerArgs p) {
         return true;
     };
     int turn = 0;
-    stream<WF, XF, 4, NT, kSteps, FULL, false>(
+    stream<WF, XF, 4, NT, kSteps, FULL, false, WF != kBf16>(
         p.H, lane, [&](U& u) { return place(u, blockIdx.x, 0); },
         [&](U& u) {
             const int4 ex = plan.act[u.id / ncol];
@@ -455,11 +456,18 @@ layer_gate_up_kernel(LayerArgs p) {
         },
         [&](const U& u, int n) {
             const int tok = plan.tok[(int)u.row0 + min(n * 16 + (lane & 15), u.rows - 1)];
-            return x_row<XF>(WF == kBf16 ? reinterpret_cast<const uint8_t*>(p.x) : p.xq, p.xqs, tok, p.H, lane);
+            if constexpr (WF == kFp4) return x_row_run(p.xq, p.xqs, tok, p.H, lane);
+            else
+                return x_row<XF>(WF == kBf16 ? reinterpret_cast<const uint8_t*>(p.x) : p.xq, p.xqs, tok, p.H,
+                                 lane);
         },
         [](const U&) {},
         [&](const v4f(&acc)[4][NT], const U& u) {
             const int64_t f0 = (int64_t)(u.id % ncol) * 32;
+            // a thread's places, computed here: kept through the stream they would
+            // take registers that it has not got
+            int me = tid;
+            asm volatile("" : "+v"(me));
             // (buffers in turn as in linear4_few_kernel)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -471,7 +479,7 @@ layer_gate_up_kernel(LayerArgs p) {
                     *reinterpret_cast<v4f*>(part + ((wave * 4 + t) * 64 + lane) * 4) = acc[t][n];
                 // thread (token, two columns f0 + 2 c, + 1): the 16 threads of a token
                 // are one DPP row and hold one block of 32
-                const int tok = tid >> 4, c = (tid & 15) * 2;
+                const int tok = me >> 4, c = (me & 15) * 2;
                 const int row = n * 16 + tok;
                 const bool live = row < u.rows;
                 const int64_t zrow = u.row0 + row;
@@ -506,9 +514,9 @@ layer_gate_up_kernel(LayerArgs p) {
                     m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x124, 0xF, 0xF, false));
                     m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x128, 0xF, 0xF, false));
                     const bool bad = m >= 0x7f800000u;
-                    const uint32_t sc = bad ? 255u : scale_code_from_amax_bits(m);
-                    const uint32_t o = bad ? 0u : e4m3x2_scaled(0u, z[0], z[1], e4m3_limit_from_code(sc),
-                                                                scale_from_code(sc), false);
+                    const uint32_t sc = bad ? 127u : scale_code_from_amax_bits(m);
+                    const uint32_t o = bad ? 0x7f7fu : e4m3x2_scaled(0u, z[0], z[1], e4m3_limit_from_code(sc),
+                                                                     scale_from_code(sc), false);
                     if (live) {
                         *reinterpret_cast<uint16_t*>(p.z + zrow * p.F + f0 + c) = (uint16_t)o;
                         if (c == 0) p.zs[zrow * (p.F / 32) + f0 / 32] = (uint8_t)sc;
@@ -538,7 +546,7 @@ constexpr size_t kLdsBytes = 160 * 1024;
 // MX weights one tile of z rows is as many bytes (MXFP4: twice) as one tile of
 // W2.  One tile: H / 16 workgroups fill the CUs and no sums of parts are left to
 // add.  Measured on 8 x (4096, 14336) MXFP4, all experts, one / two / four tiles:
-// T = 4 60 / - / - us, T = 16 92 / 68 / 67, T = 32 - / 94 / 78; 64 tokens on 64 x
+// (before its products were exact) T = 4 60 / - / - us, T = 16 92 / 68 / 67, T = 32 - / 94 / 78; 64 tokens on 64 x
 // (2048, 1408) 35 / 28 / -; bf16, 16 tokens: 155 / 156 / 170.  Past 32 tokens the
 // whole layer with two / four tiles: on 8 x (4096, 14336), top 2, MXFP4 33 tokens
 // 177 / 180 us, 64 213 / 210, MXFP8 305 / 318 and 342 / 351; on 64 x (2048, 1408),
@@ -592,7 +600,7 @@ layer_down_kernel(LayerArgs p) {
         }
         return true;
     };
-    stream<WF, XF, RT, NT, kSteps, FULL, false>(
+    stream<WF, XF, RT, NT, kSteps, FULL, false, WF != kBf16>(
         p.F, lane, [&](U& u) { return place(u, part * kDnWaves + wave, 0); },
         [&](U& u) {
             const int4 ex = plan.act[u.id / parts];
@@ -601,7 +609,9 @@ layer_down_kernel(LayerArgs p) {
             return place(u, u.id + waves, 0);
         },
         [&](const U& u, int n) {
-            return x_row<XF>(p.z, p.zs, u.row0 + min(n * 16 + (lane & 15), u.rows - 1), p.F, lane);
+            const int64_t row = u.row0 + min(n * 16 + (lane & 15), u.rows - 1);
+            if constexpr (WF == kFp4) return x_row_run(p.z, p.zs, row, p.F, lane);
+            else return x_row<XF>(p.z, p.zs, row, p.F, lane);
         },
         [](const U&) {},
         [&](const v4f(&acc)[RT][NT], const U& u) {

@@ -508,10 +508,8 @@ mx_status moe_combine_bwd(const void* dout, int64_t T, int64_t H, int32_t k,
  * that no token picks are not read.  Three launches (four where few columns of
  * out have several workgroups share the sums), no host synchronisation, one
  * fixed order of every sum (two calls give the same bits).
- * With MX weights h and the down products carry the cut of grouped_linear_fwd's
- * E4M3 products (2e-5 to 6e-5 of h in RMS), which moves some values of z to the
- * neighbouring E4M3 code: out is off by 1.7e-3 to 2.1e-3 in relative norm, where
- * its bf16 rounding alone makes 1.7e-3.
+ * Sums are fp32 of exact products with every weight format (values of MX weights
+ * past bf16's largest, which no quantizer gives, count as infinite).
  *
  *   wdtype    MX_DTYPE_BF16: w1 bf16 [E][2F][H], w2 bf16 [E][H][F], scales NULL.
  *             MX_DTYPE_MXFP8, MX_DTYPE_MXFP4: rowwise copies of the same from
