@@ -545,12 +545,13 @@ constexpr size_t kLdsBytes = 160 * 1024;
 // 16-row tiles of W2 a workgroup takes; z is read once for all of them, and for
 // MX weights one tile of z rows is as many bytes (MXFP4: twice) as one tile of
 // W2.  One tile: H / 16 workgroups fill the CUs and no sums of parts are left to
-// add.  Measured on 8 x (4096, 14336) MXFP4, all experts, one / two / four tiles:
-// (before its products were exact) T = 4 60 / - / - us, T = 16 92 / 68 / 67, T = 32 - / 94 / 78; 64 tokens on 64 x
-// (2048, 1408) 35 / 28 / -; bf16, 16 tokens: 155 / 156 / 170.  Past 32 tokens the
-// whole layer with two / four tiles: on 8 x (4096, 14336), top 2, MXFP4 33 tokens
-// 177 / 180 us, 64 213 / 210, MXFP8 305 / 318 and 342 / 351; on 64 x (2048, 1408),
-// top 8, MXFP4 79 / 76 and 81 / 85, MXFP8 115 / 115 and 123 / 122.
+// add.  Whole layer in us, one / two / four tiles: 8 x (4096, 14336), top 2, MXFP4
+// 1 token 52 / 54 / 54, 4 102 / 103 / 103, 16 155 / 151 / 153, 32 178 / 166 / 164,
+// 33 191 / 180 / 182, 64 236 / 210 / 207; MXFP8 4 155 / 157 / 157, 16 275 / 269 /
+// 267, 32 294 / 282 / 279, 33 321 / 309 / 322, 64 369 / 346 / 355; 64 x (2048,
+// 1408), top 8, MXFP4 1 25 / 25 / 30, 16 77 / 79 / 75, 32 82 / 79 / 84, 64 89 / 85 /
+// 90; MXFP8 1 28 / 29 / 32, 64 130 / 126 / 126.  bf16, 16 tokens, all experts of 8 x
+// (4096, 14336), the down projection alone: 155 / 156 / 170.
 int down_tiles(bool bf16, int64_t T, int k, int E) {
     int rt = T <= 4 || (bf16 && T <= 16) ? 1 : T <= 16 || T > 32 || bf16 ? 2 : 4;
     while (rt > 1 && down_lds(T, k, E, rt) > kLdsBytes) rt /= 2;
