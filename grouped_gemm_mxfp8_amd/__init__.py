@@ -33,6 +33,8 @@ MX_CTX_XROW, MX_CTX_W1ROW, MX_CTX_W2ROW = 6, 7, 8
 MX_WS_ZROW, MX_WS_DHROW, MX_WS_DHCOL, MX_WS_DYROW, MX_WS_DYCOL = 0, 1, 2, 3, 4
 MX_FWD_REUSE_WEIGHTS = 1
 MX_MLP_SAVE_H = 2
+MX_BWD_DW_FP32, MX_BWD_DW_ADD = 1, 2
+MX_LORA_MAX_RANK = 512
 
 _lib = None
 
@@ -48,6 +50,12 @@ _SIGS = {
     "mx_validate_offsets": (_I32, [_P, _I32, _I64]),
     "mxfp8_quantize": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _P, _I64, _P, _P]),
     "grouped_linear_fwd": (_I32, [_I32, _P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
+    "grouped_linear_bwd_ws_bytes": (_SZ, [_I32, _I64, _I64, _I64]),
+    "grouped_linear_bwd": (_I32, [_P, _P, _P, _I32, _I64, _P, _I64, _I64, _P, _P, _P, _P,
+                                  ctypes.c_uint32, _P, _SZ, _P]),
+    "lora_linear_ws_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32]),
+    "lora_linear_fwd": (_I32, [_P, _I64, _I64, _P, _I64, _P, _P, _I32, _I32, _P, _P, _P, _P, _SZ,
+                               _P]),
     "mxfp4_quantize": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
     "mxfp4_dequantize": (_I32, [_P, _P, _I64, _I64, _P, _P]),
     "moe_layer_ws_bytes": (_SZ, [_I32, _I64, _I32, _I32, _I64, _I64]),
@@ -354,6 +362,108 @@ def _linear_mxfp4(x, offsets, w: Mx4Tensor, row_scale):
         _launch("grouped_linear_fwd", dev, dtype, x.codes.data_ptr(), x.scales.data_ptr(),
                 offsets.data_ptr(), E, M, w.codes.data_ptr(), w.scales.data_ptr(), N, K,
                 0 if row_scale is None else row_scale.data_ptr(), y.data_ptr())
+    return y
+
+
+def _workspace(ws, nbytes, dev):
+    """The caller's uint8 scratch if it is large enough, else new memory."""
+    if ws is not None:
+        _need(ws, torch.uint8, "ws", dev)
+        if ws.numel() >= nbytes:
+            return ws
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def grouped_linear_bwd(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
+                       row_scale: Optional[torch.Tensor] = None,
+                       dw_dtype: torch.dtype = torch.bfloat16, dw: Optional[torch.Tensor] = None,
+                       need_dx: bool = True, need_dw: bool = True,
+                       ws: Optional[torch.Tensor] = None):
+    """Gradients of the bf16 ``grouped_linear_fwd(x, offsets, w, row_scale)`` for ``dy``
+    (bf16 [M, N]): (dx bf16 [M, K], dw [E, N, K], dr fp32 [M]).
+
+    dw is bf16 or (``dw_dtype``) fp32; with ``dw``, an fp32 tensor, the gradient is
+    added to it (it is returned).  ``need_dx`` / ``need_dw`` False: None in its place.
+    dr, the gradient of ``row_scale``, comes with dx (None without row scales).
+    ``ws``: optional caller-owned uint8 scratch (allocated when missing or too
+    small)."""
+    _need(dy, torch.bfloat16, "dy")
+    dev = dy.device
+    _need(x, torch.bfloat16, "x", dev)
+    _need(w, torch.bfloat16, "w", dev)
+    _need(offsets, torch.int64, "offsets", dev)
+    if dy.dim() != 2 or x.dim() != 2 or w.dim() != 3:
+        raise ValueError("dy must be [M, N], x [M, K] and w [E, N, K]")
+    (M, N), K, E = dy.shape, x.shape[1], w.shape[0]
+    if x.shape[0] != M or tuple(w.shape) != (E, N, K):
+        raise ValueError("shape mismatch: dy [M,N], x [M,K], w [E,N,K]")
+    if offsets.numel() != E + 1:
+        raise ValueError("offsets must have E+1 entries")
+    if row_scale is not None:
+        _need(row_scale, torch.float32, "row_scale", dev)
+        if tuple(row_scale.shape) != (M,):
+            raise ValueError("row_scale must be [M]")
+    if not (need_dx or need_dw):
+        raise ValueError("neither dx nor dw is asked for")
+    if dw is not None:
+        _need(dw, torch.float32, "dw", dev)
+        if tuple(dw.shape) != (E, N, K) or not need_dw:
+            raise ValueError("dw must be [E, N, K] (and need_dw True)")
+        flags = MX_BWD_DW_FP32 | MX_BWD_DW_ADD
+    elif dw_dtype in (torch.float32, torch.bfloat16):
+        flags = MX_BWD_DW_FP32 if dw_dtype == torch.float32 else 0
+    else:
+        raise TypeError("dw_dtype must be bfloat16 or float32")
+    nws = lib().grouped_linear_bwd_ws_bytes(E, M, N, K)
+    if nws == 0:
+        raise MxError("grouped_linear_bwd", 2, last_error())
+    ws = _workspace(ws, nws, dev)
+    if need_dw and dw is None:
+        dw = torch.empty((E, N, K), dtype=dw_dtype, device=dev)
+    dx = torch.empty_like(x) if need_dx else None
+    dr = torch.empty(M, dtype=torch.float32, device=dev) if need_dx and row_scale is not None else None
+    if M or need_dw:
+        _launch("grouped_linear_bwd", dev, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), E, M,
+                w.data_ptr(), N, K, 0 if row_scale is None or M == 0 else row_scale.data_ptr(),
+                0 if dx is None else dx.data_ptr(), 0 if dr is None else dr.data_ptr(),
+                dw.data_ptr() if need_dw else 0, flags if need_dw else 0, ws.data_ptr(), nws)
+    return dx, dw, dr
+
+
+def lora_linear_fwd(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                    ids: torch.Tensor, scale: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[m] = w @ x[m] + scale[l] * b[l] @ (a[l] @ x[m]) with l = ids[m]: a linear layer
+    shared by all rows and the low-rank adapter of each row beside it.
+
+    ``x`` bf16 [M, K], ``w`` bf16 [N, K], ``a`` bf16 [L, r, K], ``b`` bf16 [L, N, r],
+    ``ids`` int32 [M] (outside [0, L): no adapter), ``scale`` fp32 [L] (None: 1).
+    Returns bf16 [M, N].  r is a multiple of 8 up to ``MX_LORA_MAX_RANK``.  ``ws``:
+    optional caller-owned uint8 scratch (allocated when missing or too small)."""
+    _need(x, torch.bfloat16, "x")
+    dev = x.device
+    _need(w, torch.bfloat16, "w", dev)
+    _need(a, torch.bfloat16, "a", dev)
+    _need(b, torch.bfloat16, "b", dev)
+    _need(ids, torch.int32, "ids", dev)
+    if x.dim() != 2 or w.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [M, K], w [N, K], a [L, r, K] and b [L, N, r]")
+    (M, K), N, (L, r) = x.shape, w.shape[0], a.shape[:2]
+    if w.shape[1] != K or a.shape[2] != K or tuple(b.shape) != (L, N, r) or tuple(ids.shape) != (M,):
+        raise ValueError("shape mismatch: x [M,K], w [N,K], a [L,r,K], b [L,N,r], ids [M]")
+    if scale is not None:
+        _need(scale, torch.float32, "scale", dev)
+        if tuple(scale.shape) != (L,):
+            raise ValueError("scale must be [L]")
+    nws = lib().lora_linear_ws_bytes(M, N, K, L, r)
+    if nws == 0:
+        raise MxError("lora_linear_fwd", 2, last_error())
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    if M == 0:
+        return y
+    ws = _workspace(ws, nws, dev)
+    _launch("lora_linear_fwd", dev, x.data_ptr(), M, K, w.data_ptr(), N, a.data_ptr(), b.data_ptr(), L, r,
+            ids.data_ptr(), 0 if scale is None else scale.data_ptr(), y.data_ptr(), ws.data_ptr(), nws)
     return y
 
 
@@ -809,7 +919,8 @@ def moe_layer_fwd(x: torch.Tensor, logits: torch.Tensor, w1, w2, k: int,
 __all__ = ["lib", "last_error", "MxError", "MxTensor", "MlpCtx", "mxfp8_quantize",
            "Mx4Tensor", "mxfp4_quantize", "mxfp4_dequantize",
            "moe_layer_fwd",
-           "grouped_linear_fwd", "fp8_tensor_quantize", "grouped_linear_fwd_fp8", "Fp8Tensor",
+           "grouped_linear_fwd", "grouped_linear_bwd", "lora_linear_fwd",
+           "fp8_tensor_quantize", "grouped_linear_fwd_fp8", "Fp8Tensor",
            "grouped_mlp_fwd", "grouped_mlp_bwd", "padded_rows_bound",
            "ws_mx_view", "ctx_bytes", "fwd_ws_bytes", "bwd_ws_bytes", "router", "route_plan",
            "route_plan_noalloc", "permute_quantize",

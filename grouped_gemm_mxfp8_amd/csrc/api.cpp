@@ -596,6 +596,213 @@ mx_status grouped_linear_fwd(int32_t dtype, const void* x, const uint8_t* x_scal
     return launched(gemm(p, mx::Epi::kStoreBf16, 2.0 * M * N * K, s), "mx_gemm");
 }
 
+// ---- gradients of the bf16 GroupedLinear ------------------------------------------
+namespace {
+constexpr int64_t kBf16MaxDim = (int64_t)1 << 21;   // 256 rows of an operand below 2^31 bytes
+
+struct LinearBwdWs {
+    size_t scaled, drp, parts, total;
+};
+mx::Bf16Problem dgrad_problem(int32_t E, int64_t M, int64_t N, int64_t K) {
+    mx::Bf16Problem p{};
+    p.form = mx::Bf16Form::kDataGrad;
+    p.G = E;
+    p.rows = M;
+    p.M = M; p.N = K; p.K = N;
+    return p;
+}
+mx::Bf16Problem wgrad_problem(int32_t E, int64_t M, int64_t N, int64_t K) {
+    mx::Bf16Problem p{};
+    p.form = mx::Bf16Form::kWeightGrad;
+    p.G = E;
+    p.rows = M;
+    p.M = N; p.N = K; p.K = M;
+    return p;
+}
+LinearBwdWs linear_bwd_ws(int32_t E, int64_t M, int64_t N, int64_t K) {
+    Carver c;
+    LinearBwdWs L{};
+    L.scaled = c.take((size_t)(M * (N < K ? N : K)) * 2);
+    L.drp = c.take((size_t)(mx::bf16_dr_parts(K) * M) * 4);
+    const int64_t a = mx::bf16_parts(dgrad_problem(E, M, N, K)), b = mx::bf16_parts(wgrad_problem(E, M, N, K));
+    L.parts = c.take((size_t)(a > b ? a : b) * 4);
+    L.total = c.off + kAlign;
+    return L;
+}
+mx_status check_linear_bwd_sizes(int32_t E, int64_t M, int64_t N, int64_t K) {
+    if (E < 1 || E > mx::kMaxGroups || M < 0 || N <= 0 || K <= 0)
+        return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: bad sizes E=%d M=%lld N=%lld K=%lld", E, (long long)M,
+                    (long long)N, (long long)K);
+    if (K % 32 || N % 16)
+        return fail(MX_ERR_UNSUPPORTED, "grouped_linear_bwd: needs K %% 32 == 0 and N %% 16 == 0");
+    if (K > kBf16MaxDim || N > kBf16MaxDim || M > kI32Max)
+        return fail(MX_ERR_UNSUPPORTED, "grouped_linear_bwd: needs K and N up to 2^21 and M below 2^31");
+    if (mx::bf16_product_tiles(dgrad_problem(E, M, N, K)) > mx::kMaxBf16Tiles ||
+        mx::bf16_product_tiles(wgrad_problem(E, M, N, K)) > mx::kMaxBf16Tiles)
+        return fail(MX_ERR_UNSUPPORTED, "grouped_linear_bwd: too large for one launch");
+    return MX_OK;
+}
+}  // namespace
+
+size_t grouped_linear_bwd_ws_bytes(int32_t E, int64_t M, int64_t N, int64_t K) {
+    if (check_linear_bwd_sizes(E, M, N, K) != MX_OK) return 0;
+    return linear_bwd_ws(E, M, N, K).total;
+}
+
+mx_status grouped_linear_bwd(const void* dy, const void* x, const int64_t* d_offsets, int32_t E, int64_t M,
+                             const void* w, int64_t N, int64_t K, const float* d_row_scale, void* dx,
+                             float* d_dr, void* dw, uint32_t flags, void* ws, size_t ws_bytes,
+                             mx_stream_t stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const mx_status st = check_linear_bwd_sizes(E, M, N, K);
+    if (st != MX_OK) return st;
+    if (flags & ~(MX_BWD_DW_FP32 | MX_BWD_DW_ADD))
+        return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: unknown flags 0x%x", flags);
+    const bool f32 = flags & MX_BWD_DW_FP32, add = flags & MX_BWD_DW_ADD;
+    if (add && !f32) return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: only an fp32 dw is added to");
+    if (!dx && !dw) return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: neither dx nor dw is asked for");
+    if (!d_offsets || !ws || (M && !dy) || (M && dx && !w) || (M && (dw || d_dr) && !x))
+        return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: NULL argument");
+    if (d_dr && (!dx || !d_row_scale))
+        return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: dr needs row scales and dx");
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 16) || !aligned(dw, 16))
+        return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: dy, x, w, dx and dw must be 16-byte aligned");
+    if (!aligned(d_row_scale, 4) || !aligned(d_dr, 4) || !aligned(d_offsets, 8) || !aligned(ws, kAlign))
+        return fail(MX_ERR_INVALID_ARG,
+                    "grouped_linear_bwd: ws must be 256-byte, offsets 8-byte, scales and dr 4-byte aligned");
+    const LinearBwdWs L = linear_bwd_ws(E, M, N, K);
+    if (ws_bytes < L.total)
+        return fail(MX_ERR_WORKSPACE, "grouped_linear_bwd: ws has %zu bytes, needs %zu", ws_bytes, L.total);
+    const mx_status cs = check_device_offsets("grouped_linear_bwd", d_offsets, E, M, true, s);
+    if (cs != MX_OK) return cs;
+    uint8_t* const b = static_cast<uint8_t*>(ws);
+    const uint16_t *dy16 = static_cast<const uint16_t*>(dy), *x16 = static_cast<const uint16_t*>(x);
+    const double flops = 2.0 * M * N * K;
+    if (dx && M) {
+        mx::Bf16Problem p = dgrad_problem(E, M, N, K);
+        p.offs = d_offsets;
+        p.A = dy16;
+        p.B = static_cast<const uint16_t*>(w);
+        p.C = dx;
+        p.rscale = d_row_scale;
+        if (d_dr) {
+            p.drx = x16;
+            p.drp = reinterpret_cast<float*>(b + L.drp);
+            p.dr = d_dr;
+        }
+        p.parts = reinterpret_cast<float*>(b + L.parts);
+        const mx_status ls = launched(timed("linear_dgrad", flops, MX_WORK_FLOP, s,
+                                            [&] { return mx::launch_bf16_product(p, s); }),
+                                      "linear_dgrad");
+        if (ls != MX_OK) return ls;
+    }
+    if (dw && !(add && M == 0)) {
+        mx::Bf16Problem p = wgrad_problem(E, M, N, K);
+        p.offs = d_offsets;
+        p.A = dy16;
+        p.B = x16;
+        p.C = dw;
+        p.c_f32 = f32;
+        p.c_add = add;
+        p.parts = reinterpret_cast<float*>(b + L.parts);
+        if (d_row_scale && M) {
+            // the scales lie along this product's K: the narrower operand takes them,
+            // rounded to bf16 as moe_combine_bwd rounds a weighted gradient
+            uint16_t* const sc = reinterpret_cast<uint16_t*>(b + L.scaled);
+            const bool on_dy = N <= K;
+            const mx_status ls =
+                launched(timed("scale_rows", 4.0 * M * (on_dy ? N : K), MX_WORK_BYTES, s,
+                               [&] { return mx::launch_scale_rows(on_dy ? dy16 : x16, d_row_scale, M, on_dy ? N : K, sc, s); }),
+                         "scale_rows");
+            if (ls != MX_OK) return ls;
+            (on_dy ? p.A : p.B) = sc;
+        }
+        const mx_status ls = launched(timed("linear_wgrad", flops, MX_WORK_FLOP, s,
+                                            [&] { return mx::launch_bf16_product(p, s); }),
+                                      "linear_wgrad");
+        if (ls != MX_OK) return ls;
+    }
+    return ok();
+}
+
+// ---- the adapter linear -------------------------------------------------------------
+namespace {
+mx::Bf16Problem lora_problem(int64_t M, int64_t N, int64_t K) {
+    mx::Bf16Problem p{};
+    p.form = mx::Bf16Form::kForward;
+    p.G = 1;
+    p.rows = M;
+    p.M = M; p.N = N; p.K = K;
+    return p;
+}
+struct LoraWs {
+    size_t h, parts, total;
+};
+LoraWs lora_ws(int64_t M, int64_t N, int64_t K, int32_t r) {
+    Carver c;
+    LoraWs L{};
+    L.h = c.take((size_t)(M * r) * 4);
+    L.parts = c.take((size_t)mx::bf16_parts(lora_problem(M, N, K)) * 4);
+    L.total = c.off + kAlign;
+    return L;
+}
+mx_status check_lora_sizes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r) {
+    if (M < 0 || N <= 0 || K <= 0 || L < 1 || r < 1)
+        return fail(MX_ERR_INVALID_ARG, "lora_linear_fwd: bad sizes M=%lld N=%lld K=%lld L=%d r=%d", (long long)M,
+                    (long long)N, (long long)K, L, r);
+    if (K % 32 || N % 16 || r % 8)
+        return fail(MX_ERR_UNSUPPORTED, "lora_linear_fwd: needs K %% 32 == 0, N %% 16 == 0 and r %% 8 == 0");
+    if (K > kBf16MaxDim || N > kBf16MaxDim || M > kI32Max || r > MX_LORA_MAX_RANK)
+        return fail(MX_ERR_UNSUPPORTED,
+                    "lora_linear_fwd: needs K and N up to 2^21, M below 2^31 and r up to %d", MX_LORA_MAX_RANK);
+    if (mx::bf16_product_tiles(lora_problem(M, N, K)) > mx::kMaxBf16Tiles || (M + 15) / 16 > mx::kMaxBf16Tiles)
+        return fail(MX_ERR_UNSUPPORTED, "lora_linear_fwd: too large for one launch");
+    return MX_OK;
+}
+}  // namespace
+
+size_t lora_linear_ws_bytes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r) {
+    if (check_lora_sizes(M, N, K, L, r) != MX_OK) return 0;
+    return lora_ws(M, N, K, r).total;
+}
+
+mx_status lora_linear_fwd(const void* x, int64_t M, int64_t K, const void* w, int64_t N, const void* a,
+                          const void* b, int32_t L, int32_t r, const int32_t* d_ids, const float* d_scale,
+                          void* y, void* ws, size_t ws_bytes, mx_stream_t stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const mx_status st = check_lora_sizes(M, N, K, L, r);
+    if (st != MX_OK) return st;
+    if (M == 0) return ok();
+    if (!x || !w || !a || !b || !d_ids || !y || !ws)
+        return fail(MX_ERR_INVALID_ARG, "lora_linear_fwd: NULL argument");
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16))
+        return fail(MX_ERR_INVALID_ARG, "lora_linear_fwd: x, w, a, b and y must be 16-byte aligned");
+    if (!aligned(d_ids, 4) || !aligned(d_scale, 4) || !aligned(ws, kAlign))
+        return fail(MX_ERR_INVALID_ARG, "lora_linear_fwd: ws must be 256-byte, ids and scales 4-byte aligned");
+    const LoraWs W = lora_ws(M, N, K, r);
+    if (ws_bytes < W.total)
+        return fail(MX_ERR_WORKSPACE, "lora_linear_fwd: ws has %zu bytes, needs %zu", ws_bytes, W.total);
+    uint8_t* const base = static_cast<uint8_t*>(ws);
+    uint16_t* const h = reinterpret_cast<uint16_t*>(base + W.h);
+    const uint16_t* const x16 = static_cast<const uint16_t*>(x);
+    const mx_status ls = launched(timed("lora_down", 2.0 * M * r * K, MX_WORK_FLOP, s,
+                                        [&] {
+                                            return mx::launch_lora_down(x16, M, K, static_cast<const uint16_t*>(a),
+                                                                        d_ids, d_scale, L, r, h, s);
+                                        }),
+                                  "lora_down");
+    if (ls != MX_OK) return ls;
+    mx::Bf16Problem p = lora_problem(M, N, K);
+    p.A = x16;
+    p.B = static_cast<const uint16_t*>(w);
+    p.C = y;
+    p.lr = mx::LowRank{h, static_cast<const uint16_t*>(b), d_ids, r, L};
+    p.parts = reinterpret_cast<float*>(base + W.parts);
+    return launched(timed("lora_linear", 2.0 * M * N * (K + r), MX_WORK_FLOP, s,
+                          [&] { return mx::launch_bf16_product(p, s); }),
+                    "lora_linear");
+}
+
 // ---- per-tensor FP8 ------------------------------------------------------------
 mx_status fp8_tensor_quantize(const void* x, int64_t batch, int64_t R, int64_t C,
                               const int64_t* d_offsets, int32_t G, uint8_t* codes, float* d_amax,

@@ -220,6 +220,56 @@ struct LayerArgs {
 int layer_split(bool bf16, int64_t T, int k, int E, int64_t H);
 hipError_t launch_layer(LayerWeights wf, const LayerArgs& p, hipStream_t s);
 
+// ---- bf16 products: GroupedLinear's gradients, the adapter linear -----------------
+// Layout of a product C = A B^T over K: rows of A and B either K-contiguous
+// ("along") or with the output dimension contiguous ("across").
+enum class Bf16Form : int {
+    kForward = 0,      // A [M][K] along, B [N][K] along                  (y = x w^T)
+    kDataGrad = 1,     // A [M][K] along, B [G][K][N] across, rows by group (dx = dy w)
+    kWeightGrad = 2,   // A [rows][M] across, B [rows][N] across, K = a group's rows
+                       //   (dw = dy^T x), C [G][M][N]
+};
+// Low-rank adapters beside the product: row m with id[m] = l in [0, L) gets
+// h[m] b[l]^T.  h: [M][2 r] bf16, r high and r low parts of each value.
+struct LowRank {
+    const uint16_t* h;
+    const uint16_t* b;       // [L][N][r]
+    const int32_t* id;       // [M]
+    int r, L;
+};
+struct Bf16Problem {
+    Bf16Form form;
+    const int64_t* offs;     // [G + 1] groups of rows (kForward: null, one group of M)
+    int G;
+    int64_t rows;            // rows of all groups
+    int64_t M, N, K;         // of the product (kDataGrad: M = rows; kWeightGrad: K = rows)
+    const uint16_t *A, *B;
+    void* C;                 // bf16, or fp32 where c_f32
+    bool c_f32, c_add;       // c_add (fp32): added to C
+    const float* rscale;     // kDataGrad: factor of each output row, or null
+    const uint16_t* drx;     // kDataGrad with rscale: x [M][N], and
+    float* drp;              //   partial sums of x C / rscale, [bf16_dr_parts][M],
+    float* dr;               //   their sum [M] (all three null: not computed)
+    LowRank lr;              // kForward
+    float* parts;            // split sums: bf16_parts() floats
+};
+// Rows of the C matrix of each group are M of kWeightGrad, the group's rows else.
+// floats of `parts` the product takes (0: no split), workgroups of its launch (limit
+// kMaxBf16Tiles), rows of drp.
+constexpr int64_t kMaxBf16Tiles = (int64_t)1 << 23;
+int64_t bf16_product_tiles(const Bf16Problem& p);
+int64_t bf16_parts(const Bf16Problem& p);
+int64_t bf16_dr_parts(int64_t N);
+hipError_t launch_bf16_product(const Bf16Problem& p, hipStream_t s);
+// out = bf16(r[row] x), [M][C], C % 8 == 0.
+hipError_t launch_scale_rows(const uint16_t* x, const float* r, int64_t M, int64_t C, uint16_t* out,
+                             hipStream_t s);
+// h [M][2 r] = scale[id] x a[id]^T as high and low bf16 parts (rows without an
+// adapter are not written); a [L][r][K], K % 32 == 0, r % 8 == 0.
+hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, const uint16_t* a,
+                            const int32_t* id, const float* scale, int L, int r, uint16_t* h,
+                            hipStream_t s);
+
 int device_cu_count();
 
 }  // namespace mx

@@ -182,6 +182,67 @@ mx_status grouped_linear_fwd(int32_t dtype, const void* x,
                              mx_stream_t stream);
 
 /*
+ * grouped_linear_bwd -- gradients of the bf16 GroupedLinear, grouped_linear_fwd with
+ * MX_DTYPE_BF16 (y[i] = r[i] W_e x[i] for the rows i of expert e, r = 1 without
+ * row scales):
+ *   dX[i] = r[i] W_e^T dy[i]
+ *   dr[i] = x[i] . (W_e^T dy[i])
+ *   dW_e  = sum over the rows i of e of r[i] dy[i] x[i]^T
+ * Operands as they lie (no transposed copies), sums in fp32 in one fixed order (two
+ * calls give the same bits), each output rounded once; with row scales dW takes
+ * bf16(r dy) or bf16(r x), whichever is narrower, one rounding as moe_combine_bwd's
+ * weighted gradient has it.
+ *
+ *   dy bf16 [M][N], x bf16 [M][K], w bf16 [E][N][K]; d_row_scale fp32 [M] or NULL.
+ *   dx     bf16 [M][K], or NULL (not computed; w is then not read).
+ *   d_dr   fp32 [M], or NULL; needs d_row_scale and dx.
+ *   dw     bf16 [E][N][K], or NULL (not computed).  MX_BWD_DW_FP32: fp32.
+ *          MX_BWD_DW_ADD (with MX_BWD_DW_FP32): added to what dw holds, as gradients
+ *          of several micro-batches are; experts with no rows keep theirs.
+ *          Otherwise every value is written, zeros for experts with no rows.
+ *   ws     grouped_linear_bwd_ws_bytes(..) bytes of scratch, 256-byte aligned, not
+ *          shared with a call that may run at the same time.
+ * K % 32 == 0 and N % 16 == 0, both up to 2^21 (MX_ERR_UNSUPPORTED otherwise); dy, x,
+ * w, dx and dw 16-byte aligned; outputs and ws must not overlap inputs.  Nothing is
+ * allocated.  With M == 0, dy, x and dx may have no storage (dw is written).
+ */
+#define MX_BWD_DW_FP32 1u
+#define MX_BWD_DW_ADD 2u
+size_t grouped_linear_bwd_ws_bytes(int32_t E, int64_t M, int64_t N, int64_t K);
+mx_status grouped_linear_bwd(const void* dy, const void* x, const int64_t* d_offsets, int32_t E,
+                             int64_t M, const void* w, int64_t N, int64_t K,
+                             const float* d_row_scale, void* dx, float* d_dr, void* dw,
+                             uint32_t flags, void* ws, size_t ws_bytes, mx_stream_t stream);
+
+/*
+ * lora_linear_fwd -- a linear layer that all rows share and, beside it, the low-rank
+ * adapter of each row's request (serving many fine-tuned variants of one model):
+ *   y[m] = W x[m] + s[l] B_l (A_l x[m]),  l = ids[m]
+ * A row whose id is not in [0, L) has no adapter: y[m] = W x[m].  Rows come in any
+ * order; adapters' weights reach only their own rows (an infinity or NaN in one never
+ * touches another's), and a NaN in x[m] only row m.
+ *
+ *   x bf16 [M][K], w bf16 [N][K], a bf16 [L][r][K], b bf16 [L][N][r], d_ids int32 [M],
+ *   d_scale fp32 [L] or NULL (1), y bf16 [M][N].
+ *   Sums in fp32 in one fixed order; s A x goes on as two bf16 values (high and low
+ *   part, off by at most 2^-16 of it); y is rounded once.  Adapters of smaller rank: zeros in
+ *   a's further rows (or b's further columns).
+ *   K % 32 == 0, N % 16 == 0, r % 8 == 0, K and N up to 2^21, r up to
+ *   MX_LORA_MAX_RANK (MX_ERR_UNSUPPORTED otherwise); x, w, a, b and y 16-byte aligned;
+ *   y and ws must not overlap inputs.  Nothing is allocated.
+ *   ws     lora_linear_ws_bytes(..) bytes of scratch, 256-byte aligned, not shared with
+ *          a call that may run at the same time.
+ * Adapters are trained as two GroupedLinears with rows sorted by adapter (a and b as w)
+ * and their grouped_linear_bwd.
+ */
+#define MX_LORA_MAX_RANK 512
+size_t lora_linear_ws_bytes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r);
+mx_status lora_linear_fwd(const void* x, int64_t M, int64_t K, const void* w, int64_t N,
+                          const void* a, const void* b, int32_t L, int32_t r,
+                          const int32_t* d_ids, const float* d_scale, void* y, void* ws,
+                          size_t ws_bytes, mx_stream_t stream);
+
+/*
  * Per-tensor scaled FP8, the plain FP8 format the German page names beside
  * MXFP8 (paragraph on activation memory; the page gives no recipe).  Every
  * expert's slice of a grouped operand is one tensor with one fp32 scale:
