@@ -19,7 +19,7 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxmoe.so")
 SOURCES = ["api.cpp", "quantize.hip", "gemm_mxfp8.hip", "gemm_bf16.hip", "route.hip",
            "fp8_tensor.hip", "quantize_mxfp4.hip", "few_rows.hip",
-           "gemm_mxfp4.hip", "bf16_small.hip", "lora.hip"]
+           "gemm_mxfp4.hip", "bf16_small.hip", "bf16_large.hip", "lora.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

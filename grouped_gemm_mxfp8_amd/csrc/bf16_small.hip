@@ -1,11 +1,15 @@
-// bf16 products in 64 x 128 tiles (gfx950), for calls with few output tiles: the
+// bf16 products in small (64 x 128) and middle (128 x 128) tiles (gfx950), for calls with
+// few output tiles and what rounds of large ones leave, and the choice between them: the
 // data and weight gradients of GroupedLinear and the adapter linear.
 //
-// One workgroup of four waves per tile and share of K; each wave owns 32 x 64 (two
-// accumulators of the 32x32x16 MFMA).  K goes in steps of 64 through three LDS
-// stages of 24 KB filled by direct loads two steps ahead, so two workgroups share a
-// CU.  Where the tiles alone leave CUs idle, K is cut into `split` shares, whose
-// fp32 sums go to memory and are added in order by a second launch: one order of
+// One workgroup of four waves per tile and share of K; each wave owns 32 RB x 64 (RB x 2
+// accumulators of the 32x32x16 MFMA).  K goes in steps of 64 through two LDS stages
+// filled by direct loads, so two workgroups share a CU.  As in the large kernel a step's
+// fragments are in registers before it begins and its stage is refilled during it, and
+// the next step's are read into the registers that its second half's MFMAs free (read
+// where the compiler puts them, a step of a workgroup alone on its CU took 1800 cycles
+// for 512 of MFMAs).  Where the tiles alone leave CUs idle, K is cut into `split` shares,
+// whose fp32 sums go to memory and are added in order by a second launch: one order of
 // every sum, no atomics.
 //
 // LDS orders (64 banks of 4 bytes): along K, chunk c of line n is stored at
@@ -17,13 +21,20 @@
 namespace mx {
 namespace {
 
-constexpr int SM_M = 64, SM_N = 128, SM_K = 64, SM_ST = 3;
-constexpr int SM_A = SM_M * 128, SM_B = SM_N * 128, SM_STAGE = SM_A + SM_B;
-constexpr int SM_LOADS = 6;                        // per wave and step: 2 of A, 4 of B
+// MB: 32-row blocks of a wave (1: tiles of 64 x 128, 2: of 128 x 128).
+constexpr int SM_N = 128, SM_K = 64, SM_B = SM_N * 128;
+constexpr int small_m(int MB) { return 64 * MB; }
+
+// The steps' MFMAs in order: slot t is row block t / 8, sixteen t / 2 % 4 of K, column
+// block t % 2 (one that follows the one whose result it adds to would wait).  Loads go
+// one to a slot from the first half's second quarter on.
+constexpr int first_loads(int MB) { return MB == 1 ? 2 : 4; }
 
 struct SmallArgs {
     Bf16Problem p;
     int split;
+    bool lr_here;          // the tiles add the adapters' part (else the join)
+    int rounds;            // > 0: only the tiles that the large kernel with that many workgroups left
 };
 
 // Rows [k0, k0 + 64) of an operand that lies across K: base at its first column,
@@ -33,80 +44,71 @@ __device__ __forceinline__ v4i across_rsrc(const uint16_t* p, int64_t k0, int64_
     return make_rsrc(p + k0 * ld + col0, ((krows - k0) * ld - col0) * 2);
 }
 
-template <Bf16Form F>
+template <Bf16Form F, int MB>
 __global__ void __launch_bounds__(256, 2)
 bf16_small_kernel(SmallArgs s) {
+    constexpr int SM_M = small_m(MB), SM_A = SM_M * 128, SM_STAGE = SM_A + SM_B;
+    constexpr int SM_LOADS = 2 * MB + 4;                  // per wave and step, of A and B
+    constexpr int SLOTS = 8 * MB, FIRST = first_loads(MB);
     constexpr bool kA = F != Bf16Form::kWeightGrad;       // A lies along K
     constexpr bool kB = F == Bf16Form::kForward;          // B lies along K
     constexpr bool kRows = F != Bf16Form::kWeightGrad;    // groups own rows of C
     const Bf16Problem& p = s.p;
-    __shared__ __attribute__((aligned(16))) uint8_t sm[SM_ST][SM_STAGE];
-    __shared__ int s_prefix[kMaxGroups + 1];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    __shared__ __attribute__((aligned(16))) uint8_t sm[2][SM_STAGE];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     const int ntn = (int)((p.N + SM_N - 1) / SM_N);
 
     // ---- the workgroup's tile and share of K ----
-    const int share = (int)(blockIdx.x % (unsigned)s.split);
-    const int unit = (int)(blockIdx.x / (unsigned)s.split);
-    int g;
+    int g = 0;
     int64_t m0, mvalid, n0, row0 = 0, krows = p.K;
-    if constexpr (F == Bf16Form::kForward) {
-        g = 0;
-        m0 = (int64_t)(unit / ntn) * SM_M;
-        n0 = (int64_t)(unit % ntn) * SM_N;
-        mvalid = p.M - m0;
-    } else if constexpr (kRows) {
-        // row tiles of each group: prefix sums (wave 0), then the unit's group
-        if (wave == 0) {
-            int cnt[kMaxGroups / 64], local = 0;
-#pragma unroll
-            for (int u = 0; u < kMaxGroups / 64; ++u) {
-                const int i = lane * (kMaxGroups / 64) + u;
-                int c = 0;
-                if (i < p.G) {
-                    const int64_t n = p.offs[i + 1] - p.offs[i];
-                    c = n > 0 ? (int)((n + SM_M - 1) / SM_M) : 0;
-                }
-                cnt[u] = c;
-                local += c;
-            }
-            int incl = local;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(incl, d);
-                if (lane >= d) incl += o;
-            }
-            int run = incl - local;
-#pragma unroll
-            for (int u = 0; u < kMaxGroups / 64; ++u) {
-                const int i = lane * (kMaxGroups / 64) + u;
-                if (i < p.G) {
-                    s_prefix[i] = run;
-                    run += cnt[u];
-                }
-            }
-            if (lane == 63) s_prefix[p.G] = incl;
-        }
-        __syncthreads();
-        const int mt = unit / ntn;
-        if (mt >= s_prefix[p.G]) return;
-        int lo = 0, hi = p.G - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_prefix[mid] <= mt) lo = mid; else hi = mid - 1;
-        }
-        g = uni(lo);
-        m0 = uni64(p.offs[g] + (int64_t)(mt - s_prefix[g]) * SM_M);
-        n0 = (int64_t)(unit % ntn) * SM_N;
-        mvalid = uni64(p.offs[g + 1]) - m0;
+    // tiles there are (the grid is a multiple of 8 and may be larger: the rows of groups
+    // are on the device)
+    const bool rest = kRows && MB == 2 && s.rounds;       // quarters of what the large kernel left
+    const int ntl = (int)((p.N + 255) / 256);
+    int mtiles = 0, units, left = 0;
+    if constexpr (F == Bf16Form::kDataGrad)
+        mtiles = rest ? count_row_tiles<256>(p.offs, p.G, lane) : count_row_tiles<SM_M>(p.offs, p.G, lane);
+    else
+        mtiles = (int)((p.M + (rest ? 256 : SM_M) - 1) / (rest ? 256 : SM_M));
+    if (rest) {
+        left = whole_rounds(mtiles * ntl, s.rounds);
+        units = (mtiles * ntl - left) * 4;
     } else {
-        const int ntm = (int)((p.M + SM_M - 1) / SM_M);
-        g = unit / (ntm * ntn);
-        const int t = unit - g * (ntm * ntn);
-        m0 = (int64_t)(t / ntn) * SM_M;
-        n0 = (int64_t)(t % ntn) * SM_N;
+        units = mtiles * ntn * (kRows ? 1 : p.G) * s.split;
+    }
+    // workgroup b runs on XCD b % 8: each XCD takes 16 tiles of a band at a time, so that
+    // those it runs together share panels in its L2 and long sums are spread over all XCDs
+    const int nth = (int)(blockIdx.x / 8), at = nth / 16 * 128 + (int)(blockIdx.x % 8) * 16 + nth % 16;
+    if (at >= units) return;
+    const int share = at % s.split, unit = at / s.split;
+    if constexpr (kRows) {
+        RowGroup rg{0, 0, mtiles, 0, p.M};
+        int mt, nt;
+        if (rest) {
+            const int t = left + unit / 4;
+            if constexpr (F == Bf16Form::kDataGrad) rg = find_row_group<256>(p.offs, p.G, t / ntl, lane);
+            const TileAt to = band_order(t - rg.first * ntl, rg.tiles, ntl);
+            mt = to.m * 2 + (unit >> 1 & 1);
+            nt = to.n * 2 + (unit & 1);
+            if (nt >= ntn) return;
+        } else {
+            if constexpr (F == Bf16Form::kDataGrad) rg = find_row_group<SM_M>(p.offs, p.G, unit / ntn, lane);
+            const TileAt to = band_order(unit - rg.first * ntn, rg.tiles, ntn);
+            mt = to.m;
+            nt = to.n;
+        }
+        g = rg.g;
+        m0 = rg.row0 + (int64_t)mt * SM_M;
+        n0 = (int64_t)nt * SM_N;
+        mvalid = rg.rows - (int64_t)mt * SM_M;
+        if (mvalid <= 0) return;
+    } else {
+        g = unit / (mtiles * ntn);
+        const TileAt to = band_order(unit - g * (mtiles * ntn), mtiles, ntn);
+        m0 = (int64_t)to.m * SM_M;
+        n0 = (int64_t)to.n * SM_N;
         mvalid = p.M - m0;
         row0 = uni64(p.offs[g]);
         krows = uni64(p.offs[g + 1]) - row0;
@@ -125,59 +127,63 @@ bf16_small_kernel(SmallArgs s) {
     const v4i ra = make_rsrc(Ag + m0 * lda, mvalid * lda * 2);     // (along K)
     const v4i rb = make_rsrc(Bg + n0 * ldb, nvalid * ldb * 2);
     const uint32_t smb = (uint32_t)uni((int)lds_addr(sm));
-    auto load = [&](int ks) {
+    // a lane's offsets: along K 8 rows a load (odd loads' chunks are the even ones' ^ 4),
+    // across K rows of 128 MB (A) or 256 bytes
+    uint32_t aoff, boff, aflip = 0, bflip = 0;
+    const int ac = (lane & 7) ^ (lane >> 4);              // chunk of an even load along K
+    if constexpr (kA) {
+        aoff = (uint32_t)((wave * (16 * MB) + (lane >> 3)) * lda * 2) + (uint32_t)ac * 16u;
+        aflip = (ac & 4) ? (uint32_t)-64 : 64u;
+    } else {
+        const int k = wave * 16 + (MB == 1 ? lane >> 3 : lane >> 4);
+        const int c = MB == 1 ? (lane & 7) ^ (((k >> 1) & 1) << 2) : (lane & 15) ^ ((k & 3) << 2);
+        aoff = (uint32_t)(k * lda * 2) + (uint32_t)c * 16u;
+    }
+    if constexpr (kB) {
+        boff = (uint32_t)((wave * 32 + (lane >> 3)) * ldb * 2) + (uint32_t)ac * 16u;
+        bflip = (ac & 4) ? (uint32_t)-64 : 64u;
+    } else {
+        const int k = wave * 16 + (lane >> 4), c = (lane & 15) ^ ((k & 3) << 2);
+        boff = (uint32_t)(k * ldb * 2) + (uint32_t)c * 16u;
+    }
+    const uint32_t arow = (uint32_t)((kA || MB == 1 ? 8 : 4) * lda * 2), brow = (uint32_t)((kB ? 8 : 4) * ldb * 2);
+    struct Rsrc {
+        v4i a, b;
+        uint32_t soff, o0, o1;
+    };
+    // descriptors of step ks; along K the lanes whose chunk lies past K load nothing
+    auto rsrc_of = [&](int ks) -> Rsrc {
         const bool live = ks < k_end;
-        const uint32_t at = smb + (uint32_t)((ks - k_beg) % SM_ST) * SM_STAGE;
         auto rng = [&](const v4i& r) { return live ? r : v4i{r.x, r.y, 0, r.w}; };
-        const int64_t left = p.K - (int64_t)ks * SM_K;     // K values of the step (along K)
-        if constexpr (kA) {
-            static_for<2>([&](auto uc) {
-                constexpr int u = decltype(uc)::value;
-                const int row = wave * 16 + u * 8 + (lane >> 3);
-                const int c = (lane & 7) ^ ((row >> 1) & 7);
-                const uint32_t off = (uint32_t)(row * lda * 2) + (uint32_t)c * 16u;
-                dma_b128<u * 1024>(rng(ra), at + wave * 2048, off | (c * 8 < left ? 0u : 0x80000000u),
-                                   (uint32_t)ks * 128u);
-            });
+        const int64_t left = p.K - (int64_t)ks * SM_K;
+        return Rsrc{rng(kA ? ra : across_rsrc(Ag, (int64_t)ks * SM_K, krows, lda, m0)),
+                    rng(kB ? rb : across_rsrc(Bg, (int64_t)ks * SM_K, krows, ldb, n0)), (uint32_t)ks * 128u,
+                    ac * 8 < left ? 0u : 0x80000000u, (ac ^ 4) * 8 < left ? 0u : 0x80000000u};
+    };
+    auto dma = [&](auto uc, const Rsrc& r, int st) {
+        constexpr int u = decltype(uc)::value;
+        const uint32_t at = smb + (uint32_t)st * SM_STAGE;
+        if constexpr (u < 2 * MB) {
+            const uint32_t off = aoff + u * arow + (u & 1 ? aflip : 0u);
+            dma_b128<u * 1024>(r.a, at + wave * (2048 * MB), kA ? off | (u & 1 ? r.o1 : r.o0) : off, kA ? r.soff : 0u);
         } else {
-            const v4i r = rng(across_rsrc(Ag, (int64_t)ks * SM_K, krows, lda, m0));
-            static_for<2>([&](auto uc) {
-                constexpr int u = decltype(uc)::value;
-                const int k = wave * 16 + u * 8 + (lane >> 3);
-                const int c = (lane & 7) ^ (((k >> 1) & 1) << 2);
-                dma_b128<u * 1024>(r, at + wave * 2048, (uint32_t)(k * lda * 2) + (uint32_t)c * 16u, 0u);
-            });
-        }
-        if constexpr (kB) {
-            static_for<4>([&](auto uc) {
-                constexpr int u = decltype(uc)::value;
-                const int row = wave * 32 + u * 8 + (lane >> 3);
-                const int c = (lane & 7) ^ ((row >> 1) & 7);
-                const uint32_t off = (uint32_t)(row * ldb * 2) + (uint32_t)c * 16u;
-                dma_b128<u * 1024>(rng(rb), at + SM_A + wave * 4096, off | (c * 8 < left ? 0u : 0x80000000u),
-                                   (uint32_t)ks * 128u);
-            });
-        } else {
-            const v4i r = rng(across_rsrc(Bg, (int64_t)ks * SM_K, krows, ldb, n0));
-            static_for<4>([&](auto uc) {
-                constexpr int u = decltype(uc)::value;
-                const int k = wave * 16 + u * 4 + (lane >> 4);
-                const int c = (lane & 15) ^ ((k & 3) << 2);
-                dma_b128<u * 1024>(r, at + SM_A + wave * 4096, (uint32_t)(k * ldb * 2) + (uint32_t)c * 16u, 0u);
-            });
+            constexpr int v = u - 2 * MB;
+            const uint32_t off = boff + v * brow + (v & 1 ? bflip : 0u);
+            dma_b128<v * 1024>(r.b, at + SM_A + wave * 4096, kB ? off | (v & 1 ? r.o1 : r.o0) : off, kB ? r.soff : 0u);
         }
     };
 
     // ---- fragments ----
     const int l32 = lane & 31, half = lane >> 5;
-    auto frag_a = [&](const uint8_t* st, int kk) -> bf16x8 {
+    auto frag_a = [&](const uint8_t* st, int i, int kk) -> bf16x8 {
         if constexpr (kA) {
-            const int row = wm * 32 + l32;
+            const int row = wm * (32 * MB) + i * 32 + l32;
             return frag_along(st + row * 128 + (((2 * kk + half) ^ ((row >> 1) & 7)) << 4));
         } else {
             const int k = 16 * kk + 8 * half + ((lane >> 2) & 3);
-            const int c = (wm * 4 + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ (((k >> 1) & 1) << 2);
-            return frag_across(st + k * 128 + (c << 4) + 8 * (lane & 1), 4 * 128);
+            const int c = ((wm * MB + i) * 4 + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^
+                          (MB == 1 ? ((k >> 1) & 1) << 2 : (k & 3) << 2);
+            return frag_across(st + k * (128 * MB) + (c << 4) + 8 * (lane & 1), 4 * 128 * MB);
         }
     };
     auto frag_b = [&](const uint8_t* st, int j, int kk) -> bf16x8 {
@@ -191,108 +197,189 @@ bf16_small_kernel(SmallArgs s) {
         }
     };
 
-    v16f acc[2] = {zero16(), zero16()};
-    for (int ks = k_beg; ks < k_beg + SM_ST - 1; ++ks) load(ks);
-    for (int ks = k_beg; ks < k_end; ++ks) {
-        wait_vm<(SM_ST - 2) * SM_LOADS>();     // this wave's loads of step ks have landed
-        lds_barrier();                         // and everybody's; step ks - 1 is read
-        load(ks + SM_ST - 1);
-        const uint8_t* const st = sm[(ks - k_beg) % SM_ST];
+    v16f acc[MB][2];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) acc[i][0] = acc[i][1] = zero16();
+    bf16x8 af[MB][4], bf[2][4];
+    auto step = [&](int ks) {
+        const int cur = (ks - k_beg) & 1;
+        const uint8_t* const nxt = sm[cur ^ 1];
+        const Rsrc r = rsrc_of(ks + 2);
+        static_for<SLOTS>([&](auto tc) {
+            constexpr int t = decltype(tc)::value, i = t / 8, kk = t / 2 % 4, j = t % 2, q = t - SLOTS / 2;
+            if constexpr (t == SLOTS / 4) lds_barrier();      // every wave holds this step's fragments
+            if constexpr (q == 0) {
+                wait_vm<FIRST>();                             // this wave's loads of step ks + 1
+                lds_barrier();                                // and everybody's have landed
+            }
+            acc[i][j] = mfma_bf16(bf[j][kk], af[i][kk], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (t >= SLOTS / 4 && t - SLOTS / 4 < SM_LOADS)
+                dma(std::integral_constant<int, t - SLOTS / 4>{}, r, cur);
+            if constexpr (MB == 2 && q >= 0 && q < 4) af[0][q] = frag_a(nxt, 0, q);
+            if constexpr (MB == 1 && q >= 0 && q < 2) {
+                af[0][q] = frag_a(nxt, 0, q);
+                bf[0][q] = frag_b(nxt, 0, q);
+                bf[1][q] = frag_b(nxt, 1, q);
+            }
+            if constexpr (q >= 0 && j == 1) {                 // this sixteen is done with
+                af[MB - 1][kk] = frag_a(nxt, MB - 1, kk);
+                bf[0][kk] = frag_b(nxt, 0, kk);
+                bf[1][kk] = frag_b(nxt, 1, kk);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    {
+        const Rsrc r0 = rsrc_of(k_beg);
+        static_for<SM_LOADS>([&](auto uc) { dma(uc, r0, 0); });
+        if (k_beg + 1 < k_end) {
+            const Rsrc r1 = rsrc_of(k_beg + 1);
+            static_for<SM_LOADS>([&](auto uc) { dma(uc, r1, 1); });
+            wait_vm<SM_LOADS>();
+        } else {
+            wait_vm<0>();
+        }
+        lds_barrier();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-            const bf16x8 a = frag_a(st, kk);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc[j] = mfma_bf16(frag_b(st, j, kk), a, acc[j]);
+            for (int i = 0; i < MB; ++i) af[i][kk] = frag_a(sm[0], i, kk);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) bf[j][kk] = frag_b(sm[0], j, kk);
         }
     }
+    for (int ks = k_beg; ks < k_end; ++ks) step(ks);
     wait_vm<0>();          // no load may still be landing in LDS when the workgroup ends
 
-    // ---- output: the wave's 32 x 64 ----
-    const int64_t rw = m0 + wm * 32, cw = n0 + wn * 64;
-    const int rows = (int)(mvalid - wm * 32), cols = (int)(nvalid - wn * 64);
-    if (F == Bf16Form::kForward && p.lr.r && share == s.split - 1) {
-        const bool there = l32 < rows;
-        int id = there ? p.lr.id[rw + l32] : -1;
-        if (id >= p.lr.L) id = -1;
-        add_adapters<2>(acc, p.lr, there ? p.lr.h + (rw + l32) * (2 * p.lr.r) : nullptr, id, p.N, cw, lane);
-    }
+    // ---- output: the wave's blocks of 32 x 64 ----
     const int64_t gstride = kRows ? 0 : p.M * p.N;       // C of each group
-    if (s.split > 1) {
-        const int64_t all = (kRows ? p.rows : (int64_t)p.G * p.M) * p.N;
-        float* const part = p.parts + share * all + g * gstride;
+    const int64_t cw = n0 + wn * 64;
+    const int cols = (int)(nvalid - wn * 64);
+    static_for<MB>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        const int64_t rw = m0 + (wm * MB + i) * 32;
+        const int rows = (int)(mvalid - (wm * MB + i) * 32);
+        const bool there = l32 < rows;
+        v16f (&av)[2] = acc[i];
+        if (F == Bf16Form::kForward && s.lr_here && share == s.split - 1) {
+            int id = there ? p.lr.id[rw + l32] : -1;
+            if (id >= p.lr.L) id = -1;
+            add_adapters<2, 4>(av, p.lr, there ? p.lr.h + (rw + l32) * (2 * p.lr.r) : nullptr, id, p.N, cw, lane);
+        }
+        if (s.split > 1) {
+            const int64_t all = (kRows ? p.rows : (int64_t)p.G * p.M) * p.N;
+            float* const part = p.parts + share * all + g * gstride;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            store_f32_32x32<false>(acc[j], reinterpret_cast<uint8_t*>(part + rw * p.N + cw + 32 * j), p.N * 4,
-                                   rows, cols - 32 * j, lane);
-        return;
-    }
-    if constexpr (F == Bf16Form::kWeightGrad) {
-        if (p.c_f32) {
+            for (int j = 0; j < 2; ++j)
+                store_f32_32x32<false>(av[j], reinterpret_cast<uint8_t*>(part + rw * p.N + cw + 32 * j), p.N * 4,
+                                       rows, cols - 32 * j, lane);
+            return;
+        }
+        if (F == Bf16Form::kWeightGrad && p.c_f32) {
             float* const c = static_cast<float*>(p.C) + g * gstride + rw * p.N + cw;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 uint8_t* const at = reinterpret_cast<uint8_t*>(c + 32 * j);
-                if (p.c_add) store_f32_32x32<true>(acc[j], at, p.N * 4, rows, cols - 32 * j, lane);
-                else store_f32_32x32<false>(acc[j], at, p.N * 4, rows, cols - 32 * j, lane);
+                if (p.c_add) store_f32_32x32<true>(av[j], at, p.N * 4, rows, cols - 32 * j, lane);
+                else store_f32_32x32<false>(av[j], at, p.N * 4, rows, cols - 32 * j, lane);
             }
             return;
         }
-    }
-    uint8_t* const at = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.C) + g * gstride + rw * p.N + cw);
-    if (F == Bf16Form::kDataGrad && p.rscale) {
-        const bool there = l32 < rows;
-        if (p.drp && cols > 0) {
-            const uint16_t* const xr = there ? p.drx + (rw + l32) * p.N + cw : nullptr;
-            float sum = 0.f;
+        uint8_t* const at = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.C) + g * gstride + rw * p.N + cw);
+        if (F == Bf16Form::kDataGrad && p.rscale) {
+            if (p.drp && cols > 0) {
+                const uint16_t* const xr = there ? p.drx + (rw + l32) * p.N + cw : nullptr;
+                float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) sum += dot_32(acc[j], xr ? xr + 32 * j : nullptr, cols - 32 * j, lane);
-            sum += __shfl_xor(sum, 32);
-            if (there && half == 0) p.drp[(cw / 64) * p.M + rw + l32] = sum;
+                for (int j = 0; j < 2; ++j) sum += dot_32(av[j], xr ? xr + 32 * j : nullptr, cols - 32 * j, lane);
+                sum += __shfl_xor(sum, 32);
+                if (there && half == 0) p.drp[(cw / 64) * p.M + rw + l32] = sum;
+            }
+            store_bf16_32x64<true>(av[0], av[1], there ? p.rscale[rw + l32] : 0.f, at, (uint32_t)p.N * 2u, rows, cols,
+                                   lane);
+            return;
         }
-        store_bf16_32x64<true>(acc[0], acc[1], there ? p.rscale[rw + l32] : 0.f, at, (uint32_t)p.N * 2u, rows,
-                               cols, lane);
-        return;
-    }
-    store_bf16_32x64<false>(acc[0], acc[1], 1.f, at, (uint32_t)p.N * 2u, rows, cols, lane);
+        store_bf16_32x64<false>(av[0], av[1], 1.f, at, (uint32_t)p.N * 2u, rows, cols, lane);
+    });
 }
 
 // ---- sums of the shares ------------------------------------------------------------
-__device__ __forceinline__ void sum_parts8(const float* parts, int64_t all, int split, int64_t i, float (&v)[8]) {
+template <int V>           // consecutive values: 4 or 8
+__device__ __forceinline__ void sum_parts(const float* parts, int64_t all, int split, int64_t i, float (&v)[V]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    for (int e = 0; e < V; ++e) v[e] = 0.f;
+#pragma unroll 8
     for (int c = 0; c < split; ++c) {
         const float4* q = reinterpret_cast<const float4*>(parts + c * all + i);
-        const float4 a = q[0], b = q[1];
-        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+            const float4 a = q[e / 4];
+            v[e] += a.x; v[e + 1] += a.y; v[e + 2] += a.z; v[e + 3] += a.w;
+        }
     }
 }
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
 }
 
-// Eight values a thread.
+// Four values a thread.
 __global__ void __launch_bounds__(256)
 bf16_join_kernel(const float* __restrict__ parts, int64_t all, int split, void* __restrict__ c, bool f32,
                  bool add) {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= all) return;
-    float v[8];
-    sum_parts8(parts, all, split, i, v);
+    float v[4];
+    sum_parts(parts, all, split, i, v);
     if (!f32) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c) + i) = pack8(v);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c) + i) = pack4_bf16(v);
         return;
     }
-    float* const out = static_cast<float*>(c) + i;
-#pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-        float4 y = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        if (add) {
-            const float4 o = *reinterpret_cast<const float4*>(out + e);
-            y = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
-        }
-        *reinterpret_cast<float4*>(out + e) = y;
+    float4* const out = reinterpret_cast<float4*>(static_cast<float*>(c) + i);
+    float4 y = make_float4(v[0], v[1], v[2], v[3]);
+    if (add) {
+        const float4 o = *out;
+        y = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
     }
+    *out = y;
+}
+
+// Four columns of a row a thread (rows by grid.y), with the adapters' part: each value
+// the dot of the row's h with its adapter's row of b, r at a time of eight.
+__global__ void __launch_bounds__(256)
+bf16_join_adapters_kernel(const float* __restrict__ parts, int64_t M, int64_t N, int split, LowRank lr,
+                          uint16_t* __restrict__ c) {
+    const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, m = blockIdx.y;
+    if (n >= N) return;
+    const int id = lr.id[m], r = lr.r;
+    float low[4] = {0.f, 0.f, 0.f, 0.f};
+    if (id >= 0 && id < lr.L) {
+        const uint16_t* const h = lr.h + m * (2 * r);
+        const uint16_t* const b = lr.b + ((int64_t)id * N + n) * r;
+#pragma unroll 2
+        for (int k = 0; k < r; k += 8) {
+            const uint4 hi = *reinterpret_cast<const uint4*>(h + k), lo = *reinterpret_cast<const uint4*>(h + r + k);
+            const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
+            uint4 bv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bv[e] = *reinterpret_cast<const uint4*>(b + e * r + k);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float h0 = bf16_to_f32(hw[q] & 0xffffu) + bf16_to_f32(lw[q] & 0xffffu);
+                const float h1 = __uint_as_float(hw[q] & 0xffff0000u) + __uint_as_float(lw[q] & 0xffff0000u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t w = q == 0 ? bv[e].x : q == 1 ? bv[e].y : q == 2 ? bv[e].z : bv[e].w;
+                    low[e] += h0 * bf16_to_f32(w & 0xffffu) + h1 * __uint_as_float(w & 0xffff0000u);
+                }
+            }
+        }
+    }
+    float v[4];
+    sum_parts(parts, M * N, split, m * N + n, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += low[e];
+    *reinterpret_cast<uint2*>(c + m * N + n) = pack4_bf16(v);
 }
 
 // One row a workgroup, with its factor and (dr given) dr[row] = x . (the row without it).
@@ -305,7 +392,7 @@ bf16_join_rows_kernel(const float* __restrict__ parts, int64_t M, int64_t N, int
     float sum = 0.f;
     for (int64_t n = threadIdx.x * 8; n < N; n += 2048) {
         float v[8];
-        sum_parts8(parts, M * N, split, row * N + n, v);
+        sum_parts(parts, M * N, split, row * N + n, v);
         uint4 xv = make_uint4(0, 0, 0, 0);
         if (dr) xv = *reinterpret_cast<const uint4*>(x + row * N + n);
         const uint32_t w[4] = {xv.x, xv.y, xv.z, xv.w};
@@ -350,53 +437,160 @@ scale_rows_kernel(const uint16_t* __restrict__ x, const float* __restrict__ r, i
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tiles of a call (an upper bound where groups own rows: their counts are on the device).
-int64_t small_tiles(const Bf16Problem& p) {
-    const int64_t ntn = cdiv(p.N, SM_N);
-    if (p.form == Bf16Form::kForward) return cdiv(p.M, SM_M) * ntn;
-    if (p.form == Bf16Form::kDataGrad)       // sum of ceil(rows / 64) <= this
-        return (p.rows < p.G ? p.rows : p.G + (p.rows - p.G) / SM_M) * ntn;
-    return (int64_t)p.G * cdiv(p.M, SM_M) * ntn;
+int64_t small_tiles(const Bf16Problem& p, int MB) {
+    const int64_t ntn = cdiv(p.N, SM_N), bm = small_m(MB);
+    if (p.form == Bf16Form::kForward) return cdiv(p.M, bm) * ntn;
+    if (p.form == Bf16Form::kDataGrad)       // sum of ceil(rows / bm) <= this
+        return (p.rows < p.G ? p.rows : p.G + (p.rows - p.G) / bm) * ntn;
+    return (int64_t)p.G * cdiv(p.M, bm) * ntn;
 }
 
-int small_split(const Bf16Problem& p) {
-    const int64_t tiles = small_tiles(p);
-    // a group's steps of K, by the average
-    const int64_t nk = cdiv(p.form == Bf16Form::kWeightGrad ? cdiv(p.rows, p.G) : p.K, SM_K);
-    int64_t split = tiles ? 512 / tiles : 1;
-    if (split > nk / 4) split = nk / 4;
-    return split < 1 ? 1 : split > 16 ? 16 : (int)split;
+// ---- which kernel ------------------------------------------------------------------
+enum Kind { kLarge = 0, kSmall = 1, kMiddle = 2 };     // (kSmall, kMiddle: also MB)
+struct Plan {
+    Kind kind;
+    int split;
+};
+
+// Rows of groups are on the device: groups are taken as equal here.
+//
+// Products whose groups own rows: the fastest by a model of their times, in us, its
+// numbers measured at K x N of 4096 x 4096, 1408 x 2064, 4096 x 14336 and 1024 x 1024
+// with 17 to 8192 rows, and at 1 to 64 experts with 4 to 4096 rows each.  A tile's step
+// of 64 in K takes a CU 0.45 (small) or 0.75 (middle) for a workgroup alone, 0.35 or 0.52
+// a workgroup when it has several, and 1.6 (large, four middle ones' work); starting and
+// storing take 6, a large round 12 in all; adding the shares of a split K takes 4.5 and
+// the time its bytes need.  A last round of large tiles goes to middle ones where
+// whole_rounds says so.
+Plan plan_rows(const Bf16Problem& p) {
+    const int64_t groups = p.form == Bf16Form::kForward ? 1 : p.rows < p.G ? p.rows : p.G;
+    const int64_t rows = groups ? cdiv(p.rows, groups) : 0;
+    const double nk = (double)cdiv(p.K, SM_K);
+    auto tiles = [&](int bm, int bn) { return (double)(groups * cdiv(rows, bm) * cdiv(p.N, bn)); };
+    auto tile_us = [&](Kind k, double units, double steps) {
+        const double each = units / 256;
+        return each <= 1 ? steps * (k == kSmall ? 0.45 : 0.75) : steps * (k == kSmall ? 0.35 : 0.52) * (each < 2 ? 2 : each);
+    };
+    Plan best{kSmall, 1};
+    double least = 1e30;
+    for (Kind k : {kSmall, kMiddle}) {
+        const double t = tiles(small_m(k), SM_N);
+        for (int split = 1; split <= 16 && nk >= 4.0 * split && t * split <= 1024; ++split) {
+            double us = 6 + tile_us(k, t * split, nk / split);
+            if (split > 1) us += 4.5 + 8e-6 * split * p.rows * p.N / 3;
+            if (us < least) {
+                least = us;
+                best = Plan{k, split};
+            }
+        }
+        if (t > 1024 && 6 + tile_us(k, t, nk) < least) {
+            least = 6 + tile_us(k, t, nk);
+            best = Plan{k, 1};
+        }
+    }
+    const double t = tiles(256, 256);
+    if (t < 1e9) {
+        const int whole = whole_rounds((int)t, 256), rest = (int)t - whole;
+        const double us = cdiv(whole, 256) * 1.6 * nk + (whole ? 12 : 0) + (rest ? 6 + tile_us(kMiddle, 4.0 * rest, nk) : 0);
+        if (whole && us < least) best = Plan{kLarge, 1};
+    } else {
+        best = Plan{kLarge, 1};
+    }
+    return best;
 }
+
+// Weight gradients: the large tiles' chains hide the stores that take most of the time
+// where groups have few rows, but a few rounds of them wait for the group with most rows
+// (8 experts of 2816 x 1024, 16384 rows falling as 1 / rank^1.1: 174 us, middle tiles
+// 113; even: 112 and 111).  One group has no such thing, only a last round partly used
+// (4096 x 4096, 2048 rows: 59 us, middle 75).  Middle tiles split long sums where there
+// are few (8 of 512 x 512, 16384 rows: 27 us, large 52).
+Plan plan_weights(const Bf16Problem& p) {
+    const int64_t large = p.G * cdiv(p.M, 256) * cdiv(p.N, 256);
+    const int64_t last = large % 256;
+    if (large >= 1024 || (p.G == 1 && large >= 192 && (last == 0 || last >= 192))) return Plan{kLarge, 1};
+    const int64_t tiles = p.G * cdiv(p.M, small_m(kMiddle)) * cdiv(p.N, SM_N);
+    const int64_t nk = cdiv(cdiv(p.rows, p.G), SM_K);
+    // a share keeps 16 steps
+    int64_t split = 512 / tiles;
+    if (split > nk / 16) split = nk / 16;
+    return Plan{kMiddle, split < 1 ? 1 : split > 16 ? 16 : (int)split};
+}
+
+Plan plan_of(const Bf16Problem& p) {
+    return p.form == Bf16Form::kWeightGrad ? plan_weights(p) : plan_rows(p);
+}
+
+// Workgroups of the small or middle tiles of a call.
+int64_t small_grid(const Bf16Problem& p, const Plan& q) { return cdiv(small_tiles(p, q.kind) * q.split, 128) * 128; }
 
 }  // namespace
 
 int64_t bf16_parts(const Bf16Problem& p) {
-    const int split = small_split(p);
-    return split > 1 ? split * (p.form == Bf16Form::kWeightGrad ? (int64_t)p.G * p.M : p.rows) * p.N : 0;
+    const Plan q = plan_of(p);
+    return q.split > 1 ? q.split * (p.form == Bf16Form::kWeightGrad ? (int64_t)p.G * p.M : p.rows) * p.N : 0;
 }
 
-int64_t bf16_product_tiles(const Bf16Problem& p) { return small_tiles(p) * small_split(p); }
+int64_t bf16_product_tiles(const Bf16Problem& p) {
+    const Plan q = plan_of(p);
+    return q.kind == kLarge ? small_tiles(p, kMiddle) / 128 : small_grid(p, q);
+}
 
 int64_t bf16_dr_parts(int64_t N) { return cdiv(N, 64); }
 
 hipError_t launch_bf16_product(const Bf16Problem& p, hipStream_t st) {
-    SmallArgs a{p, small_split(p)};
-    const int64_t grid = small_tiles(p) * a.split;
+    const Plan q = plan_of(p);
+    if (q.kind == kLarge) {
+        const bool tail = p.form != Bf16Form::kWeightGrad;
+        hipError_t e = launch_bf16_large(p, tail, st);
+        if (e != hipSuccess) return e;
+        if (tail) {
+            const SmallArgs t{p, 1, true, bf16_large_grid()};
+            const dim3 tg((4 * kTailMost + 127) / 128 * 128), tb(256);
+            if (p.form == Bf16Form::kForward)
+                hipLaunchKernelGGL((bf16_small_kernel<Bf16Form::kForward, 2>), tg, tb, 0, st, t);
+            else
+                hipLaunchKernelGGL((bf16_small_kernel<Bf16Form::kDataGrad, 2>), tg, tb, 0, st, t);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        if (p.drp) return launch_dr_reduce(p.drp, p.M, bf16_dr_parts(p.N), p.dr, st);
+        return hipSuccess;
+    }
+    SmallArgs a{p, q.split, false, 0};
+    if (p.form == Bf16Form::kForward && p.M <= kLoraFewRows)
+        return launch_lora_few(p.A, p.M, p.K, p.B, p.N, p.lr, static_cast<uint16_t*>(p.C), st);
+    // The adapters' part in the tiles shares each adapter's b among up to 32 rows, in the
+    // join every row reads its own.
+    const bool join_lr = p.form == Bf16Form::kForward && a.split > 1 && p.M * p.N * p.lr.r <= (int64_t)1 << 25;
+    a.lr_here = !join_lr;
+    const int64_t grid = small_grid(p, q);
     if (grid == 0) return hipSuccess;
     const dim3 gd((unsigned)grid), bd(256);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, gd, bd, 0, st, a); };
+    const bool small = q.kind == kSmall;
     switch (p.form) {
-        case Bf16Form::kForward: hipLaunchKernelGGL(bf16_small_kernel<Bf16Form::kForward>, gd, bd, 0, st, a); break;
-        case Bf16Form::kDataGrad: hipLaunchKernelGGL(bf16_small_kernel<Bf16Form::kDataGrad>, gd, bd, 0, st, a); break;
-        default: hipLaunchKernelGGL(bf16_small_kernel<Bf16Form::kWeightGrad>, gd, bd, 0, st, a);
+        case Bf16Form::kForward:
+            small ? go(bf16_small_kernel<Bf16Form::kForward, 1>) : go(bf16_small_kernel<Bf16Form::kForward, 2>);
+            break;
+        case Bf16Form::kDataGrad:
+            small ? go(bf16_small_kernel<Bf16Form::kDataGrad, 1>) : go(bf16_small_kernel<Bf16Form::kDataGrad, 2>);
+            break;
+        default:
+            go(bf16_small_kernel<Bf16Form::kWeightGrad, 2>);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (a.split > 1) {
-        if (p.rscale) {
+        if (join_lr) {
+            hipLaunchKernelGGL(bf16_join_adapters_kernel, dim3((unsigned)cdiv(p.N, 1024), (unsigned)p.M), bd, 0, st,
+                               p.parts, p.M, p.N, a.split, p.lr, static_cast<uint16_t*>(p.C));
+        } else if (p.rscale) {
             hipLaunchKernelGGL(bf16_join_rows_kernel, dim3((unsigned)p.M), bd, 0, st, p.parts, p.M, p.N, a.split,
                                p.rscale, p.drx, static_cast<uint16_t*>(p.C), p.dr);
         } else {
             const int64_t all = (p.form == Bf16Form::kWeightGrad ? (int64_t)p.G * p.M : p.rows) * p.N;
-            hipLaunchKernelGGL(bf16_join_kernel, dim3((unsigned)cdiv(all, 2048)), bd, 0, st, p.parts, all, a.split,
+            hipLaunchKernelGGL(bf16_join_kernel, dim3((unsigned)cdiv(all, 1024)), bd, 0, st, p.parts, all, a.split,
                                p.C, p.c_f32, p.c_add);
         }
         return hipGetLastError();

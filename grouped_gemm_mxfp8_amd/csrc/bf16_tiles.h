@@ -38,6 +38,79 @@ __device__ __forceinline__ v16f mfma_bf16(const bf16x8& cols, const bf16x8& rows
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(cols, rows, c, 0, 0, 0);
 }
 
+// ---- tiles ------------------------------------------------------------------------
+// Groups of rows [offs[g], offs[g + 1]) in tiles of BM rows, group after group: how many
+// tiles there are, and the group of one.  A wave does this with a lane per group.
+template <int BM>
+__device__ __forceinline__ int row_tiles(int64_t beg, int64_t end) {
+    return end > beg ? (int)((end - beg + BM - 1) / BM) : 0;
+}
+__device__ __forceinline__ int wave_prefix(int v, int lane) {          // inclusive
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+template <int BM>
+__device__ __forceinline__ int count_row_tiles(const int64_t* offs, int G, int lane) {
+    int n = 0;
+    for (int c = 0; c < G; c += 64)
+        if (c + lane < G) n += row_tiles<BM>(offs[c + lane], offs[c + lane + 1]);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d);
+    return uni(n);
+}
+struct RowGroup {
+    int g, first, tiles;      // group (-1: there is no such tile), its first tile, how many it has
+    int64_t row0, rows;
+};
+template <int BM>
+__device__ __forceinline__ RowGroup find_row_group(const int64_t* offs, int G, int tile, int lane) {
+    int base = 0;
+    for (int c = 0; c < G; c += 64) {
+        const int g = c + lane;
+        const int64_t beg = g < G ? offs[g] : 0, end = g < G ? offs[g + 1] : 0;
+        const int cnt = row_tiles<BM>(beg, end), incl = base + wave_prefix(cnt, lane);
+        const uint64_t after = __ballot(incl > tile);
+        if (after) {
+            const int l = __builtin_ctzll(after);
+            auto at = [&](int64_t v) {
+                const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, l);
+                const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)v >> 32), l);
+                return (int64_t)(((uint64_t)hi << 32) | lo);
+            };
+            const int n = __builtin_amdgcn_readlane(cnt, l);
+            const int64_t row0 = at(beg);
+            return RowGroup{uni(c + l), __builtin_amdgcn_readlane(incl, l) - n, n, row0, at(end) - row0};
+        }
+        base = __builtin_amdgcn_readlane(incl, 63);
+    }
+    return RowGroup{-1, 0, 0, 0, 0};
+}
+
+// The large kernel's order of a group's tiles: bands of BAND row tiles, so that the tiles
+// an XCD runs together share panels of both operands in its L2.
+constexpr int BAND = 8;
+struct TileAt {
+    int m, n;
+};
+__device__ __forceinline__ TileAt band_order(int local, int mtiles, int ntn) {
+    const int band = local / (BAND * ntn);
+    const int rem = local - band * BAND * ntn;
+    const int bm = min(BAND, mtiles - band * BAND);
+    return TileAt{band * BAND + rem % bm, rem / bm};
+}
+
+// Rounds of the large kernel.  It runs `grid` tiles at a time; a last round of up to
+// kTailMost tiles is left to the middle tiles, four to a large one, two at a time on a CU.
+constexpr int kTailMost = 176;
+__device__ __host__ __forceinline__ int whole_rounds(int tiles, int grid) {
+    const int rest = tiles % grid;
+    return rest <= kTailMost ? tiles - rest : tiles;
+}
+
 // Fragment of an operand staged along K: 16 bytes.
 __device__ __forceinline__ bf16x8 frag_along(const uint8_t* p) {
     return __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(p));
@@ -180,48 +253,62 @@ __device__ __forceinline__ float dot_32(const v16f& a, const uint16_t* xr, int c
 // rows' own adapters: h b^T with h as two bf16 values (hi + lo) a number.  lane l:
 // row l & 31, id its adapter or negative, hrow its h (hi values, then lo values,
 // r each; null for a row that does not exist).  b: [.][N][r]; col: the wave's first
-// column, cols how many exist.  One product per adapter among the rows, from zero,
-// and only that adapter's rows take it: what another adapter's weights hold, NaN
-// included, never meets a row.
-template <int NB>
+// column.  Each adapter among the rows is multiplied for itself, sixteen ranks at a
+// time from zero, and only its own rows take the result: what another adapter's
+// weights hold, NaN included, never meets a row.  U products' operands are in flight
+// together (one by one, 32 rows of 32 adapters took 16 us of loads' latency).
+template <int NB, int U>
 __device__ __forceinline__ void add_adapters(v16f (&acc)[NB], const LowRank& lr, const uint16_t* hrow, int id,
                                              int64_t N, int64_t col, int lane) {
     const int half = lane >> 5, r = lr.r;
     uint64_t left = __ballot(hrow != nullptr && id >= 0);
+    int k = 0;
     while (left) {
-        const int one = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        const bool mine = hrow != nullptr && id == one;
-        const uint16_t* const b = lr.b + (int64_t)one * N * r;
-        v16f t[NB];
+        uint4 hi[U], lo[U], bv[U][NB];
+        int who[U];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) t[j] = zero16();
-        for (int k = 0; k < r; k += 16) {
+        for (int u = 0; u < U; ++u) {
+            who[u] = -1;
+            if (left == 0) continue;
+            const int one = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+            who[u] = one;
+            const bool mine = hrow != nullptr && id == one;
             const int kl = k + 8 * half;
-            uint4 hi = make_uint4(0, 0, 0, 0), lo = hi, bv[NB];
+            hi[u] = lo[u] = make_uint4(0, 0, 0, 0);
             if (mine && kl < r) {
-                hi = *reinterpret_cast<const uint4*>(hrow + kl);
-                lo = *reinterpret_cast<const uint4*>(hrow + r + kl);
+                hi[u] = *reinterpret_cast<const uint4*>(hrow + kl);
+                lo[u] = *reinterpret_cast<const uint4*>(hrow + r + kl);
             }
+            const uint16_t* const b = lr.b + (int64_t)one * N * r + kl;
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 const int64_t n = col + 32 * j + (lane & 31);
-                bv[j] = make_uint4(0, 0, 0, 0);
-                if (n < N && kl < r) bv[j] = *reinterpret_cast<const uint4*>(b + n * r + kl);
+                bv[u][j] = make_uint4(0, 0, 0, 0);
+                if (n < N && kl < r) bv[u][j] = *reinterpret_cast<const uint4*>(b + n * r);
             }
+            k += 16;
+            if (k >= r) {
+                k = 0;
+                left &= ~__ballot(mine);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (who[u] < 0) continue;
+            v16f t[NB];
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                const bf16x8 bf = __builtin_bit_cast(bf16x8, bv[j]);
-                t[j] = mfma_bf16(bf, __builtin_bit_cast(bf16x8, hi), t[j]);
-                t[j] = mfma_bf16(bf, __builtin_bit_cast(bf16x8, lo), t[j]);
+                const bf16x8 bf = __builtin_bit_cast(bf16x8, bv[u][j]);
+                t[j] = mfma_bf16(bf, __builtin_bit_cast(bf16x8, hi[u]), zero16());
+                t[j] = mfma_bf16(bf, __builtin_bit_cast(bf16x8, lo[u]), t[j]);
+            }
+            if (hrow != nullptr && id == who[u]) {
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[j][v] += t[j][v];
             }
         }
-        if (mine) {
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) acc[j][v] += t[j][v];
-        }
-        left &= ~__ballot(mine);
     }
 }
 

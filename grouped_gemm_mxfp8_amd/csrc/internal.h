@@ -260,6 +260,10 @@ constexpr int64_t kMaxBf16Tiles = (int64_t)1 << 23;
 int64_t bf16_product_tiles(const Bf16Problem& p);
 int64_t bf16_parts(const Bf16Problem& p);
 int64_t bf16_dr_parts(int64_t N);
+// The kernels it chooses from: 256 x 256 tiles (tail: only whole rounds of them, see
+// whole_rounds; the rest is then the middle tiles'), bf16_large_grid() workgroups.
+int bf16_large_grid();
+hipError_t launch_bf16_large(const Bf16Problem& p, bool tail, hipStream_t s);
 hipError_t launch_bf16_product(const Bf16Problem& p, hipStream_t s);
 // out = bf16(r[row] x), [M][C], C % 8 == 0.
 hipError_t launch_scale_rows(const uint16_t* x, const float* r, int64_t M, int64_t C, uint16_t* out,
@@ -269,6 +273,10 @@ hipError_t launch_scale_rows(const uint16_t* x, const float* r, int64_t M, int64
 hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, const uint16_t* a,
                             const int32_t* id, const float* scale, int L, int r, uint16_t* h,
                             hipStream_t s);
+// y [M][N] = x w^T + the adapters' part for up to kLoraFewRows rows, N % 16 == 0.
+constexpr int kLoraFewRows = 16;
+hipError_t launch_lora_few(const uint16_t* x, int64_t M, int64_t K, const uint16_t* w, int64_t N, const LowRank& lr,
+                           uint16_t* y, hipStream_t s);
 
 int device_cu_count();
 

@@ -80,8 +80,16 @@ SHAPES = [
 ]
 
 
+# enough tiles for the large kernel: whole rounds of 256 and what is left of them, sums
+# of one, two and three steps, ragged edges on every side
+LARGE = [
+    ([4097], 16, 4128), ([2500, 0, 3, 1700, 300], 80, 4096), ([4000, 130, 257], 208, 4384),
+    ([900, 0, 5000, 129], 144, 4640), ([0, 70, 129, 700, 0, 1], 2064, 2848), ([1500, 10], 4112, 3616),
+]
+
+
 @pytest.mark.parametrize("scaled", [False, True])
-@pytest.mark.parametrize("counts,N,K", SHAPES)
+@pytest.mark.parametrize("counts,N,K", SHAPES + LARGE)
 def test_against_fp64(dev, counts, N, K, scaled):
     dy, x, w, off, offd, r = make(counts, N, K, N + K, dev, scaled)
     nws = gm.lib().grouped_linear_bwd_ws_bytes(len(counts), x.shape[0], N, K)
