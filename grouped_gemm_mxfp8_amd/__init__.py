@@ -50,7 +50,7 @@ _SIGS = {
     "mx_validate_offsets": (_I32, [_P, _I32, _I64]),
     "mxfp8_quantize": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _P, _I64, _P, _P]),
     "grouped_linear_fwd": (_I32, [_I32, _P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
-    "grouped_linear_bwd_ws_bytes": (_SZ, [_I32, _I64, _I64, _I64]),
+    "grouped_linear_bwd_ws_bytes": (_SZ, [_I32, _I64, _I64, _I64, _I32]),
     "grouped_linear_bwd": (_I32, [_P, _P, _P, _I32, _I64, _P, _I64, _I64, _P, _P, _P, _P,
                                   ctypes.c_uint32, _P, _SZ, _P]),
     "lora_linear_ws_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32]),
@@ -366,7 +366,10 @@ def _linear_mxfp4(x, offsets, w: Mx4Tensor, row_scale):
 
 
 def _workspace(ws, nbytes, dev):
-    """The caller's uint8 scratch if it is large enough, else new memory."""
+    """The caller's uint8 scratch if it is large enough, else new memory (None where
+    256 bytes, which stand for none, are asked for)."""
+    if nbytes <= 256:
+        return None
     if ws is not None:
         _need(ws, torch.uint8, "ws", dev)
         if ws.numel() >= nbytes:
@@ -414,7 +417,7 @@ def grouped_linear_bwd(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
         flags = MX_BWD_DW_FP32 if dw_dtype == torch.float32 else 0
     else:
         raise TypeError("dw_dtype must be bfloat16 or float32")
-    nws = lib().grouped_linear_bwd_ws_bytes(E, M, N, K)
+    nws = lib().grouped_linear_bwd_ws_bytes(E, M, N, K, row_scale is not None)
     if nws == 0:
         raise MxError("grouped_linear_bwd", 2, last_error())
     ws = _workspace(ws, nws, dev)
@@ -426,7 +429,8 @@ def grouped_linear_bwd(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
         _launch("grouped_linear_bwd", dev, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), E, M,
                 w.data_ptr(), N, K, 0 if row_scale is None or M == 0 else row_scale.data_ptr(),
                 0 if dx is None else dx.data_ptr(), 0 if dr is None else dr.data_ptr(),
-                dw.data_ptr() if need_dw else 0, flags if need_dw else 0, ws.data_ptr(), nws)
+                dw.data_ptr() if need_dw else 0, flags if need_dw else 0,
+                0 if ws is None else ws.data_ptr(), nws)
     return dx, dw, dr
 
 
@@ -463,7 +467,8 @@ def lora_linear_fwd(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.
         return y
     ws = _workspace(ws, nws, dev)
     _launch("lora_linear_fwd", dev, x.data_ptr(), M, K, w.data_ptr(), N, a.data_ptr(), b.data_ptr(), L, r,
-            ids.data_ptr(), 0 if scale is None else scale.data_ptr(), y.data_ptr(), ws.data_ptr(), nws)
+            ids.data_ptr(), 0 if scale is None else scale.data_ptr(), y.data_ptr(),
+            0 if ws is None else ws.data_ptr(), nws)
     return y
 
 

@@ -600,8 +600,11 @@ mx_status grouped_linear_fwd(int32_t dtype, const void* x, const uint8_t* x_scal
 namespace {
 constexpr int64_t kBf16MaxDim = (int64_t)1 << 21;   // 256 rows of an operand below 2^31 bytes
 
+// Size of a scratch buffer with `used` bytes of regions: kAlign stands for none at all.
+size_t needed_or_none(size_t used) { return kAlign + used; }
+
 struct LinearBwdWs {
-    size_t scaled, drp, parts, total;
+    size_t scaled, drp, dparts, wparts, total;
 };
 mx::Bf16Problem dgrad_problem(int32_t E, int64_t M, int64_t N, int64_t K) {
     mx::Bf16Problem p{};
@@ -619,14 +622,14 @@ mx::Bf16Problem wgrad_problem(int32_t E, int64_t M, int64_t N, int64_t K) {
     p.M = N; p.N = K; p.K = M;
     return p;
 }
-LinearBwdWs linear_bwd_ws(int32_t E, int64_t M, int64_t N, int64_t K) {
+LinearBwdWs linear_bwd_ws(int32_t E, int64_t M, int64_t N, int64_t K, bool scaled) {
     Carver c;
     LinearBwdWs L{};
-    L.scaled = c.take((size_t)(M * (N < K ? N : K)) * 2);
-    L.drp = c.take((size_t)(mx::bf16_dr_parts(K) * M) * 4);
-    const int64_t a = mx::bf16_parts(dgrad_problem(E, M, N, K)), b = mx::bf16_parts(wgrad_problem(E, M, N, K));
-    L.parts = c.take((size_t)(a > b ? a : b) * 4);
-    L.total = c.off + kAlign;
+    L.scaled = c.take(scaled ? (size_t)(M * (N < K ? N : K)) * 2 : 0);
+    L.drp = c.take(scaled ? (size_t)(mx::bf16_dr_parts(K) * M) * 4 : 0);
+    L.dparts = c.take((size_t)mx::bf16_parts(dgrad_problem(E, M, N, K)) * 4);
+    L.wparts = c.take((size_t)mx::bf16_parts(wgrad_problem(E, M, N, K)) * 4);
+    L.total = needed_or_none(c.off);
     return L;
 }
 mx_status check_linear_bwd_sizes(int32_t E, int64_t M, int64_t N, int64_t K) {
@@ -644,9 +647,9 @@ mx_status check_linear_bwd_sizes(int32_t E, int64_t M, int64_t N, int64_t K) {
 }
 }  // namespace
 
-size_t grouped_linear_bwd_ws_bytes(int32_t E, int64_t M, int64_t N, int64_t K) {
+size_t grouped_linear_bwd_ws_bytes(int32_t E, int64_t M, int64_t N, int64_t K, int32_t scaled) {
     if (check_linear_bwd_sizes(E, M, N, K) != MX_OK) return 0;
-    return linear_bwd_ws(E, M, N, K).total;
+    return linear_bwd_ws(E, M, N, K, scaled != 0).total;
 }
 
 mx_status grouped_linear_bwd(const void* dy, const void* x, const int64_t* d_offsets, int32_t E, int64_t M,
@@ -661,7 +664,7 @@ mx_status grouped_linear_bwd(const void* dy, const void* x, const int64_t* d_off
     const bool f32 = flags & MX_BWD_DW_FP32, add = flags & MX_BWD_DW_ADD;
     if (add && !f32) return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: only an fp32 dw is added to");
     if (!dx && !dw) return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: neither dx nor dw is asked for");
-    if (!d_offsets || !ws || (M && !dy) || (M && dx && !w) || (M && (dw || d_dr) && !x))
+    if (!d_offsets || (M && !dy) || (M && dx && !w) || (M && (dw || d_dr) && !x))
         return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: NULL argument");
     if (d_dr && (!dx || !d_row_scale))
         return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: dr needs row scales and dx");
@@ -670,59 +673,50 @@ mx_status grouped_linear_bwd(const void* dy, const void* x, const int64_t* d_off
     if (!aligned(d_row_scale, 4) || !aligned(d_dr, 4) || !aligned(d_offsets, 8) || !aligned(ws, kAlign))
         return fail(MX_ERR_INVALID_ARG,
                     "grouped_linear_bwd: ws must be 256-byte, offsets 8-byte, scales and dr 4-byte aligned");
-    const LinearBwdWs L = linear_bwd_ws(E, M, N, K);
-    if (ws_bytes < L.total)
+    const LinearBwdWs L = linear_bwd_ws(E, M, N, K, d_row_scale != nullptr);
+    if (L.total > kAlign && !ws) return fail(MX_ERR_INVALID_ARG, "grouped_linear_bwd: NULL ws");
+    if (L.total > kAlign && ws_bytes < L.total)
         return fail(MX_ERR_WORKSPACE, "grouped_linear_bwd: ws has %zu bytes, needs %zu", ws_bytes, L.total);
     const mx_status cs = check_device_offsets("grouped_linear_bwd", d_offsets, E, M, true, s);
     if (cs != MX_OK) return cs;
     uint8_t* const b = static_cast<uint8_t*>(ws);
     const uint16_t *dy16 = static_cast<const uint16_t*>(dy), *x16 = static_cast<const uint16_t*>(x);
-    const double flops = 2.0 * M * N * K;
-    if (dx && M) {
-        mx::Bf16Problem p = dgrad_problem(E, M, N, K);
-        p.offs = d_offsets;
-        p.A = dy16;
-        p.B = static_cast<const uint16_t*>(w);
-        p.C = dx;
-        p.rscale = d_row_scale;
+    mx::Bf16Problem d = dgrad_problem(E, M, N, K), g = wgrad_problem(E, M, N, K);
+    const bool with_dx = dx && M, with_dw = dw && !(add && M == 0);
+    if (with_dx) {
+        d.offs = d_offsets;
+        d.A = dy16;
+        d.B = static_cast<const uint16_t*>(w);
+        d.C = dx;
+        d.rscale = d_row_scale;
         if (d_dr) {
-            p.drx = x16;
-            p.drp = reinterpret_cast<float*>(b + L.drp);
-            p.dr = d_dr;
+            d.drx = x16;
+            d.drp = reinterpret_cast<float*>(b + L.drp);
+            d.dr = d_dr;
         }
-        p.parts = reinterpret_cast<float*>(b + L.parts);
-        const mx_status ls = launched(timed("linear_dgrad", flops, MX_WORK_FLOP, s,
-                                            [&] { return mx::launch_bf16_product(p, s); }),
-                                      "linear_dgrad");
-        if (ls != MX_OK) return ls;
+        d.parts = reinterpret_cast<float*>(b + L.dparts);
     }
-    if (dw && !(add && M == 0)) {
-        mx::Bf16Problem p = wgrad_problem(E, M, N, K);
-        p.offs = d_offsets;
-        p.A = dy16;
-        p.B = x16;
-        p.C = dw;
-        p.c_f32 = f32;
-        p.c_add = add;
-        p.parts = reinterpret_cast<float*>(b + L.parts);
-        if (d_row_scale && M) {
-            // the scales lie along this product's K: the narrower operand takes them,
-            // rounded to bf16 as moe_combine_bwd rounds a weighted gradient
-            uint16_t* const sc = reinterpret_cast<uint16_t*>(b + L.scaled);
-            const bool on_dy = N <= K;
-            const mx_status ls =
-                launched(timed("scale_rows", 4.0 * M * (on_dy ? N : K), MX_WORK_BYTES, s,
-                               [&] { return mx::launch_scale_rows(on_dy ? dy16 : x16, d_row_scale, M, on_dy ? N : K, sc, s); }),
-                         "scale_rows");
-            if (ls != MX_OK) return ls;
-            (on_dy ? p.A : p.B) = sc;
-        }
-        const mx_status ls = launched(timed("linear_wgrad", flops, MX_WORK_FLOP, s,
-                                            [&] { return mx::launch_bf16_product(p, s); }),
-                                      "linear_wgrad");
-        if (ls != MX_OK) return ls;
+    const bool scaled = with_dw && d_row_scale && M, on_dy = N <= K;
+    uint16_t* const copy = scaled ? reinterpret_cast<uint16_t*>(b + L.scaled) : nullptr;
+    if (with_dw) {
+        g.offs = d_offsets;
+        g.A = dy16;
+        g.B = x16;
+        // the scales lie along this product's K: the narrower operand takes them, rounded
+        // to bf16 as moe_combine_bwd rounds a weighted gradient
+        if (scaled) (on_dy ? g.A : g.B) = copy;
+        g.C = dw;
+        g.c_f32 = f32;
+        g.c_add = add;
+        g.parts = reinterpret_cast<float*>(b + L.wparts);
     }
-    return ok();
+    if (!with_dx && !with_dw) return ok();
+    return launched(timed("linear_bwd", 2.0 * M * N * K * (with_dx + with_dw), MX_WORK_FLOP, s,
+                          [&] {
+                              return mx::launch_linear_grads(with_dx ? &d : nullptr, with_dw ? &g : nullptr,
+                                                             on_dy ? dy16 : x16, d_row_scale, on_dy ? N : K, copy, s);
+                          }),
+                    "linear_bwd");
 }
 
 // ---- the adapter linear -------------------------------------------------------------
@@ -736,15 +730,18 @@ mx::Bf16Problem lora_problem(int64_t M, int64_t N, int64_t K) {
     return p;
 }
 struct LoraWs {
-    size_t h, parts, total;
+    size_t h, order, ids, parts, total;
 };
-LoraWs lora_ws(int64_t M, int64_t N, int64_t K, int32_t r) {
+LoraWs lora_ws(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r) {
     Carver c;
-    LoraWs L{};
-    L.h = c.take((size_t)(M * r) * 4);
-    L.parts = c.take((size_t)mx::bf16_parts(lora_problem(M, N, K)) * 4);
-    L.total = c.off + kAlign;
-    return L;
+    LoraWs W{};
+    const size_t sorted = mx::lora_sorts(M, K, L) ? (size_t)M * 4 : 0;
+    W.h = c.take(M > mx::kLoraFewRows || !mx::lora_fuses(M, r) ? (size_t)(M * r) * 4 : 0);
+    W.order = c.take(sorted);
+    W.ids = c.take(sorted);
+    W.parts = c.take(M > mx::kLoraFewRows ? (size_t)mx::bf16_parts(lora_problem(M, N, K)) * 4 : 0);
+    W.total = needed_or_none(c.off);
+    return W;
 }
 mx_status check_lora_sizes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r) {
     if (M < 0 || N <= 0 || K <= 0 || L < 1 || r < 1)
@@ -755,7 +752,7 @@ mx_status check_lora_sizes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r
     if (K > kBf16MaxDim || N > kBf16MaxDim || M > kI32Max || r > MX_LORA_MAX_RANK)
         return fail(MX_ERR_UNSUPPORTED,
                     "lora_linear_fwd: needs K and N up to 2^21, M below 2^31 and r up to %d", MX_LORA_MAX_RANK);
-    if (mx::bf16_product_tiles(lora_problem(M, N, K)) > mx::kMaxBf16Tiles || (M + 15) / 16 > mx::kMaxBf16Tiles)
+    if (mx::bf16_product_tiles(lora_problem(M, N, K)) > mx::kMaxBf16Tiles || (M + 15) / 16 > mx::kMaxBf16Tiles / 2)
         return fail(MX_ERR_UNSUPPORTED, "lora_linear_fwd: too large for one launch");
     return MX_OK;
 }
@@ -763,7 +760,7 @@ mx_status check_lora_sizes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r
 
 size_t lora_linear_ws_bytes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r) {
     if (check_lora_sizes(M, N, K, L, r) != MX_OK) return 0;
-    return lora_ws(M, N, K, r).total;
+    return lora_ws(M, N, K, L, r).total;
 }
 
 mx_status lora_linear_fwd(const void* x, int64_t M, int64_t K, const void* w, int64_t N, const void* a,
@@ -773,33 +770,52 @@ mx_status lora_linear_fwd(const void* x, int64_t M, int64_t K, const void* w, in
     const mx_status st = check_lora_sizes(M, N, K, L, r);
     if (st != MX_OK) return st;
     if (M == 0) return ok();
-    if (!x || !w || !a || !b || !d_ids || !y || !ws)
+    if (!x || !w || !a || !b || !d_ids || !y)
         return fail(MX_ERR_INVALID_ARG, "lora_linear_fwd: NULL argument");
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16))
         return fail(MX_ERR_INVALID_ARG, "lora_linear_fwd: x, w, a, b and y must be 16-byte aligned");
     if (!aligned(d_ids, 4) || !aligned(d_scale, 4) || !aligned(ws, kAlign))
         return fail(MX_ERR_INVALID_ARG, "lora_linear_fwd: ws must be 256-byte, ids and scales 4-byte aligned");
-    const LoraWs W = lora_ws(M, N, K, r);
-    if (ws_bytes < W.total)
+    const LoraWs W = lora_ws(M, N, K, L, r);
+    if (W.total > kAlign && !ws) return fail(MX_ERR_INVALID_ARG, "lora_linear_fwd: NULL ws");
+    if (W.total > kAlign && ws_bytes < W.total)
         return fail(MX_ERR_WORKSPACE, "lora_linear_fwd: ws has %zu bytes, needs %zu", ws_bytes, W.total);
     uint8_t* const base = static_cast<uint8_t*>(ws);
     uint16_t* const h = reinterpret_cast<uint16_t*>(base + W.h);
     const uint16_t* const x16 = static_cast<const uint16_t*>(x);
-    const mx_status ls = launched(timed("lora_down", 2.0 * M * r * K, MX_WORK_FLOP, s,
-                                        [&] {
-                                            return mx::launch_lora_down(x16, M, K, static_cast<const uint16_t*>(a),
-                                                                        d_ids, d_scale, L, r, h, s);
-                                        }),
-                                  "lora_down");
-    if (ls != MX_OK) return ls;
+    const uint16_t *const a16 = static_cast<const uint16_t*>(a), *const w16 = static_cast<const uint16_t*>(w);
+    mx::LowRank lr{h, static_cast<const uint16_t*>(b), d_ids, r, L, nullptr};
+    const double flops = 2.0 * M * N * (K + r);
+    mx_status ls;
+    if (mx::lora_sorts(M, K, L)) {
+        int32_t *const to = reinterpret_cast<int32_t*>(base + W.order), *const sid = reinterpret_cast<int32_t*>(base + W.ids);
+        ls = launched(timed("lora_sort", 16.0 * M, MX_WORK_BYTES, s,
+                            [&] { return mx::launch_lora_sort(d_ids, M, L, to, sid, s); }),
+                      "lora_sort");
+        if (ls != MX_OK) return ls;
+        lr.id = sid;
+        lr.order = to;
+    }
+    if (M > mx::kLoraFewRows || !mx::lora_fuses(M, r)) {
+        ls = launched(timed("lora_down", 2.0 * M * r * K, MX_WORK_FLOP, s,
+                            [&] { return mx::launch_lora_down(x16, M, K, a16, lr.id, lr.order, d_scale, L, r, h, s); }),
+                      "lora_down");
+        if (ls != MX_OK) return ls;
+    }
+    if (M <= mx::kLoraFewRows)
+        return launched(timed("lora_few", flops, MX_WORK_FLOP, s,
+                              [&] {
+                                  return mx::launch_lora_few(x16, M, K, w16, N, lr, a16, d_scale,
+                                                             static_cast<uint16_t*>(y), s);
+                              }),
+                        "lora_few");
     mx::Bf16Problem p = lora_problem(M, N, K);
     p.A = x16;
-    p.B = static_cast<const uint16_t*>(w);
+    p.B = w16;
     p.C = y;
-    p.lr = mx::LowRank{h, static_cast<const uint16_t*>(b), d_ids, r, L};
+    p.lr = lr;
     p.parts = reinterpret_cast<float*>(base + W.parts);
-    return launched(timed("lora_linear", 2.0 * M * N * (K + r), MX_WORK_FLOP, s,
-                          [&] { return mx::launch_bf16_product(p, s); }),
+    return launched(timed("lora_linear", flops, MX_WORK_FLOP, s, [&] { return mx::launch_lora_product(p, s); }),
                     "lora_linear");
 }
 

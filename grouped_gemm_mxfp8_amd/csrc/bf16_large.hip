@@ -179,6 +179,10 @@ bf16_large_kernel(Bf16Problem p, bool leave_tail) {
         } else {
             s.a = reinterpret_cast<const uint8_t*>(a + t.m0 * lda);
             s.an = t.mvalid * lda * 2;
+            if (F == Bf16Form::kForward && p.lr.order) {
+                s.a = reinterpret_cast<const uint8_t*>(a);
+                s.an = p.M * lda * 2;
+            }
             if constexpr (F == Bf16Form::kDataGrad) {
                 s.b = reinterpret_cast<const uint8_t*>(b + (int64_t)t.g * p.K * p.N + t.n0);
                 s.bn = (p.K * p.N - t.n0) * 2;
@@ -196,6 +200,23 @@ bf16_large_kernel(Bf16Problem p, bool leave_tail) {
         Tile L = locate(w);
         bool pre = false;
         int base = 0;          // stage of the tile's step 0
+        // (rows of A in another order: each load's own offsets, kept for the whole tile and
+        // set to the next one's when its loads begin; a row past the last loads nothing)
+        constexpr bool kOrder = OUT == Out::kAdapters;
+        uint32_t ro[kOrder ? 8 : 1];
+        auto rows_of = [&](const Tile& t) {
+            if constexpr (kOrder) {
+                const int ln = lane_now();
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int row = wave * 64 + u * 8 + (ln >> 3);
+                    const int64_t from = !p.lr.order ? row : row < t.mvalid ? p.lr.order[t.m0 + row] : -1;
+                    ro[u] = (from < 0 ? 0x80000000u : (uint32_t)(from * lda * 2)) +
+                            (uint32_t)(((ln & 7) ^ (ln >> 4)) ^ (u & 1 ? 4 : 0)) * 16u;
+                }
+            }
+        };
+        rows_of(L);
         for (;;) {
             const int wnext = w + grid;
             const bool has_next = wnext < total;
@@ -241,7 +262,9 @@ bf16_large_kernel(Bf16Problem p, bool leave_tail) {
             auto dma = [&](auto uc, const Rsrc& r, int st) {
                 constexpr int u = decltype(uc)::value;
                 if constexpr (u < 8) {
-                    const uint32_t off = aoff + (uint32_t)(u * (kA ? 8 : 2) * lda * 2) + (u & 1 ? aflip : 0u);
+                    uint32_t off;
+                    if constexpr (kOrder) off = ro[u];
+                    else off = aoff + (uint32_t)(u * (kA ? 8 : 2) * lda * 2) + (u & 1 ? aflip : 0u);
                     dma_b128<u * 1024>(r.a, smb + (uint32_t)offsetof(Smem, a) + st * STAGE + wave * 8192,
                                        TAIL && kA ? off | (u & 1 ? r.o1 : r.o0) : off, kA ? r.soff : 0u);
                 } else {
@@ -360,6 +383,7 @@ bf16_large_kernel(Bf16Problem p, bool leave_tail) {
             if (has_next) {
                 Ln = locate(wnext);
                 nx = src_of(Ln);
+                if (kOrder && p.lr.order) rows_of(Ln);    // (the tile's own loads are all issued)
             }
             for (; ks < nk; ++ks) step(ks, nx, ks + 2 - nk, std::false_type{}, std::false_type{});
 
@@ -369,6 +393,30 @@ bf16_large_kernel(Bf16Problem p, bool leave_tail) {
                 const int64_t rw = L.m0 + wm * 128, cw = L.n0 + wn * 128;
                 const int rows = (int)(L.mvalid - wm * 128), cols = (int)min((int64_t)128, p.N - cw);
                 const int64_t at = (kRows ? 0 : (int64_t)L.g * p.M * p.N) + rw * p.N + cw;
+                int to[kOrder ? 4 : 1][4];
+                if constexpr (kOrder) {
+                    // all adapters' parts before the first store, whose completion the loads
+                    // of the next part would wait for
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) line_rows(to[i], p.lr.order, rw + 32 * i, rows - 32 * i, ln);
+                    static_for<4>([&](auto ic) {
+                        constexpr int i = decltype(ic)::value;
+                        const int64_t row = rw + 32 * i + (ln & 31);
+                        const bool there = (ln & 31) < rows - 32 * i;
+                        int id = there ? p.lr.id[row] : -1;
+                        if (id >= p.lr.L) id = -1;
+                        const uint16_t* const hr = there ? p.lr.h + row * (2 * p.lr.r) : nullptr;
+                        // half the columns at a time: what one adapter adds needs registers
+                        // of its own
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            v16f part[2] = {acc[i][2 * h], acc[i][2 * h + 1]};
+                            add_adapters<2, 2>(part, p.lr, hr, id, p.N, cw + 64 * h, ln);
+                            acc[i][2 * h] = part[0];
+                            acc[i][2 * h + 1] = part[1];
+                        }
+                    });
+                }
                 static_for<4>([&](auto ic) {
                     constexpr int i = decltype(ic)::value;
                     const int r0 = rows - 32 * i;
@@ -385,20 +433,6 @@ bf16_large_kernel(Bf16Problem p, bool leave_tail) {
                         const int64_t row = rw + 32 * i + (ln & 31);
                         const bool there = (ln & 31) < r0;
                         float sc = 1.f;
-                        if constexpr (OUT == Out::kAdapters) {
-                            int id = there ? p.lr.id[row] : -1;
-                            if (id >= p.lr.L) id = -1;
-                            const uint16_t* const hr = there ? p.lr.h + row * (2 * p.lr.r) : nullptr;
-                            // half the columns at a time: what one adapter adds needs registers
-                            // of its own
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                v16f part[2] = {acc[i][2 * h], acc[i][2 * h + 1]};
-                                add_adapters<2, 2>(part, p.lr, hr, id, p.N, cw + 64 * h, ln);
-                                acc[i][2 * h] = part[0];
-                                acc[i][2 * h + 1] = part[1];
-                            }
-                        }
                         if constexpr (OUT == Out::kScaled) {
                             sc = s_rsw[wave * 128 + 32 * i + (ln & 31)];
                             if (p.drp) {
@@ -418,7 +452,12 @@ bf16_large_kernel(Bf16Problem p, bool leave_tail) {
                         uint8_t* const c = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.C) + at + 32 * i * p.N);
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            store_bf16_32x64<OUT == Out::kScaled>(acc[i][2 * h], acc[i][2 * h + 1], sc, c + 128 * h,
+                            if constexpr (kOrder)
+                                store_bf16_32x64<false, true>(
+                                    acc[i][2 * h], acc[i][2 * h + 1], 1.f,
+                                    reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.C) + cw + 64 * h),
+                                    (uint32_t)p.N * 2u, r0, cols - 64 * h, ln, to[i]);
+                            else store_bf16_32x64<OUT == Out::kScaled>(acc[i][2 * h], acc[i][2 * h + 1], sc, c + 128 * h,
                                                                   (uint32_t)p.N * 2u, r0, cols - 64 * h, ln);
                     }
                     // one row block at a time (read ahead, later blocks would spill)

@@ -13,9 +13,8 @@
 // every sum, no atomics.
 //
 // LDS orders (64 banks of 4 bytes): along K, chunk c of line n is stored at
-// c ^ (n >> 1 & 7); across K, the 64-byte quarter of a row at quarter ^ (k & 3)
-// (256-byte rows) or ^ (k >> 1 & 1) (128-byte rows), so that the rows that one
-// transposing read takes lie on different banks.
+// c ^ (n >> 1 & 7); across K, the 64-byte quarter of a 256-byte row at quarter ^ (k & 3),
+// so that the rows that one transposing read takes lie on different banks.
 #include "bf16_tiles.h"
 
 namespace mx {
@@ -44,17 +43,19 @@ __device__ __forceinline__ v4i across_rsrc(const uint16_t* p, int64_t k0, int64_
     return make_rsrc(p + k0 * ld + col0, ((krows - k0) * ld - col0) * 2);
 }
 
+constexpr int small_stage(int MB) { return small_m(MB) * 128 + SM_B; }
+
+// What workgroup `block` (of a multiple of 128) of a product's does.
 template <Bf16Form F, int MB>
-__global__ void __launch_bounds__(256, 2)
-bf16_small_kernel(SmallArgs s) {
-    constexpr int SM_M = small_m(MB), SM_A = SM_M * 128, SM_STAGE = SM_A + SM_B;
+__device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
+                                           uint8_t (&sm)[2][small_stage(MB)]) {
+    constexpr int SM_M = small_m(MB), SM_A = SM_M * 128, SM_STAGE = small_stage(MB);
     constexpr int SM_LOADS = 2 * MB + 4;                  // per wave and step, of A and B
     constexpr int SLOTS = 8 * MB, FIRST = first_loads(MB);
     constexpr bool kA = F != Bf16Form::kWeightGrad;       // A lies along K
     constexpr bool kB = F == Bf16Form::kForward;          // B lies along K
     constexpr bool kRows = F != Bf16Form::kWeightGrad;    // groups own rows of C
     const Bf16Problem& p = s.p;
-    __shared__ __attribute__((aligned(16))) uint8_t sm[2][SM_STAGE];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
@@ -80,7 +81,7 @@ bf16_small_kernel(SmallArgs s) {
     }
     // workgroup b runs on XCD b % 8: each XCD takes 16 tiles of a band at a time, so that
     // those it runs together share panels in its L2 and long sums are spread over all XCDs
-    const int nth = (int)(blockIdx.x / 8), at = nth / 16 * 128 + (int)(blockIdx.x % 8) * 16 + nth % 16;
+    const int nth = block / 8, at = nth / 16 * 128 + block % 8 * 16 + nth % 16;
     if (at >= units) return;
     const int share = at % s.split, unit = at / s.split;
     if constexpr (kRows) {
@@ -124,20 +125,29 @@ bf16_small_kernel(SmallArgs s) {
     const uint16_t* const Bg = F == Bf16Form::kDataGrad ? p.B + (int64_t)g * p.K * p.N
                                : F == Bf16Form::kWeightGrad ? p.B + row0 * p.N : p.B;
     const uint16_t* const Ag = F == Bf16Form::kWeightGrad ? p.A + row0 * p.M : p.A;
-    const v4i ra = make_rsrc(Ag + m0 * lda, mvalid * lda * 2);     // (along K)
+    // (along K; the adapter linear may take its rows in another order)
+    const int32_t* const order = F == Bf16Form::kForward ? p.lr.order : nullptr;
+    const v4i ra = order ? make_rsrc(Ag, p.M * lda * 2) : make_rsrc(Ag + m0 * lda, mvalid * lda * 2);
     const v4i rb = make_rsrc(Bg + n0 * ldb, nvalid * ldb * 2);
     const uint32_t smb = (uint32_t)uni((int)lds_addr(sm));
     // a lane's offsets: along K 8 rows a load (odd loads' chunks are the even ones' ^ 4),
-    // across K rows of 128 MB (A) or 256 bytes
-    uint32_t aoff, boff, aflip = 0, bflip = 0;
+    // across K rows of 256 bytes
+    uint32_t aoff[2 * MB], boff, bflip = 0;
     const int ac = (lane & 7) ^ (lane >> 4);              // chunk of an even load along K
     if constexpr (kA) {
-        aoff = (uint32_t)((wave * (16 * MB) + (lane >> 3)) * lda * 2) + (uint32_t)ac * 16u;
-        aflip = (ac & 4) ? (uint32_t)-64 : 64u;
+#pragma unroll
+        for (int u = 0; u < 2 * MB; ++u) {
+            const int row = wave * (16 * MB) + u * 8 + (lane >> 3);
+            const int64_t from = !order ? row : row < mvalid ? order[m0 + row] : -1;
+            aoff[u] = (from < 0 ? 0x80000000u : (uint32_t)(from * lda * 2)) + (uint32_t)(ac ^ (u & 1 ? 4 : 0)) * 16u;
+        }
     } else {
-        const int k = wave * 16 + (MB == 1 ? lane >> 3 : lane >> 4);
-        const int c = MB == 1 ? (lane & 7) ^ (((k >> 1) & 1) << 2) : (lane & 15) ^ ((k & 3) << 2);
-        aoff = (uint32_t)(k * lda * 2) + (uint32_t)c * 16u;
+        static_assert(kA || MB == 2, "256-byte rows of A across K");
+#pragma unroll
+        for (int u = 0; u < 2 * MB; ++u) {
+            const int k = wave * 16 + u * 4 + (lane >> 4), c = (lane & 15) ^ ((k & 3) << 2);
+            aoff[u] = (uint32_t)(k * lda * 2) + (uint32_t)c * 16u;
+        }
     }
     if constexpr (kB) {
         boff = (uint32_t)((wave * 32 + (lane >> 3)) * ldb * 2) + (uint32_t)ac * 16u;
@@ -146,7 +156,7 @@ bf16_small_kernel(SmallArgs s) {
         const int k = wave * 16 + (lane >> 4), c = (lane & 15) ^ ((k & 3) << 2);
         boff = (uint32_t)(k * ldb * 2) + (uint32_t)c * 16u;
     }
-    const uint32_t arow = (uint32_t)((kA || MB == 1 ? 8 : 4) * lda * 2), brow = (uint32_t)((kB ? 8 : 4) * ldb * 2);
+    const uint32_t brow = (uint32_t)((kB ? 8 : 4) * ldb * 2);
     struct Rsrc {
         v4i a, b;
         uint32_t soff, o0, o1;
@@ -164,8 +174,8 @@ bf16_small_kernel(SmallArgs s) {
         constexpr int u = decltype(uc)::value;
         const uint32_t at = smb + (uint32_t)st * SM_STAGE;
         if constexpr (u < 2 * MB) {
-            const uint32_t off = aoff + u * arow + (u & 1 ? aflip : 0u);
-            dma_b128<u * 1024>(r.a, at + wave * (2048 * MB), kA ? off | (u & 1 ? r.o1 : r.o0) : off, kA ? r.soff : 0u);
+            dma_b128<u * 1024>(r.a, at + wave * (2048 * MB), kA ? aoff[u] | (u & 1 ? r.o1 : r.o0) : aoff[u],
+                               kA ? r.soff : 0u);
         } else {
             constexpr int v = u - 2 * MB;
             const uint32_t off = boff + v * brow + (v & 1 ? bflip : 0u);
@@ -181,9 +191,8 @@ bf16_small_kernel(SmallArgs s) {
             return frag_along(st + row * 128 + (((2 * kk + half) ^ ((row >> 1) & 7)) << 4));
         } else {
             const int k = 16 * kk + 8 * half + ((lane >> 2) & 3);
-            const int c = ((wm * MB + i) * 4 + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^
-                          (MB == 1 ? ((k >> 1) & 1) << 2 : (k & 3) << 2);
-            return frag_across(st + k * (128 * MB) + (c << 4) + 8 * (lane & 1), 4 * 128 * MB);
+            const int c = ((wm * 2 + i) * 4 + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ ((k & 3) << 2);
+            return frag_across(st + k * 256 + (c << 4) + 8 * (lane & 1), 4 * 256);
         }
     };
     auto frag_b = [&](const uint8_t* st, int j, int kk) -> bf16x8 {
@@ -300,8 +309,22 @@ bf16_small_kernel(SmallArgs s) {
                                    lane);
             return;
         }
-        store_bf16_32x64<false>(av[0], av[1], 1.f, at, (uint32_t)p.N * 2u, rows, cols, lane);
+        if constexpr (F == Bf16Form::kForward) {
+            int to[4];
+            line_rows(to, order, rw, rows, lane);
+            store_bf16_32x64<false, true>(av[0], av[1], 1.f, reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.C) + cw),
+                                          (uint32_t)p.N * 2u, rows, cols, lane, to);
+        } else {
+            store_bf16_32x64<false>(av[0], av[1], 1.f, at, (uint32_t)p.N * 2u, rows, cols, lane);
+        }
     });
+}
+
+template <int MB>
+__global__ void __launch_bounds__(256, 2)
+bf16_forward_kernel(SmallArgs s) {
+    __shared__ __attribute__((aligned(16))) uint8_t sm[2][small_stage(MB)];
+    small_tile<Bf16Form::kForward, MB>(s, (int)blockIdx.x, sm);
 }
 
 // ---- sums of the shares ------------------------------------------------------------
@@ -344,42 +367,49 @@ bf16_join_kernel(const float* __restrict__ parts, int64_t all, int split, void* 
     *out = y;
 }
 
-// Four columns of a row a thread (rows by grid.y), with the adapters' part: each value
-// the dot of the row's h with its adapter's row of b, r at a time of eight.
+// Four columns of a row a thread (rows by grid.y), for the adapter linear: rows to where
+// they belong, and (ADAPTERS) the adapters' part, each value the dot of the row's h with
+// its adapter's row of b.
+template <bool ADAPTERS>
 __global__ void __launch_bounds__(256)
 bf16_join_adapters_kernel(const float* __restrict__ parts, int64_t M, int64_t N, int split, LowRank lr,
                           uint16_t* __restrict__ c) {
-    const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, m = blockIdx.y;
+    const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (n >= N) return;
-    const int id = lr.id[m], r = lr.r;
-    float low[4] = {0.f, 0.f, 0.f, 0.f};
-    if (id >= 0 && id < lr.L) {
-        const uint16_t* const h = lr.h + m * (2 * r);
-        const uint16_t* const b = lr.b + ((int64_t)id * N + n) * r;
+    for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
+        float low[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (ADAPTERS) {
+            const int id = lr.id[m], r = lr.r;
+            if (id >= 0 && id < lr.L) {
+                const uint16_t* const h = lr.h + m * (2 * r);
+                const uint16_t* const b = lr.b + ((int64_t)id * N + n) * r;
 #pragma unroll 2
-        for (int k = 0; k < r; k += 8) {
-            const uint4 hi = *reinterpret_cast<const uint4*>(h + k), lo = *reinterpret_cast<const uint4*>(h + r + k);
-            const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
-            uint4 bv[4];
+                for (int k = 0; k < r; k += 8) {
+                    const uint4 hi = *reinterpret_cast<const uint4*>(h + k), lo = *reinterpret_cast<const uint4*>(h + r + k);
+                    const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
+                    uint4 bv[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) bv[e] = *reinterpret_cast<const uint4*>(b + e * r + k);
+                    for (int e = 0; e < 4; ++e) bv[e] = *reinterpret_cast<const uint4*>(b + e * r + k);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float h0 = bf16_to_f32(hw[q] & 0xffffu) + bf16_to_f32(lw[q] & 0xffffu);
-                const float h1 = __uint_as_float(hw[q] & 0xffff0000u) + __uint_as_float(lw[q] & 0xffff0000u);
+                    for (int q = 0; q < 4; ++q) {
+                        const float h0 = bf16_to_f32(hw[q] & 0xffffu) + bf16_to_f32(lw[q] & 0xffffu);
+                        const float h1 = __uint_as_float(hw[q] & 0xffff0000u) + __uint_as_float(lw[q] & 0xffff0000u);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t w = q == 0 ? bv[e].x : q == 1 ? bv[e].y : q == 2 ? bv[e].z : bv[e].w;
-                    low[e] += h0 * bf16_to_f32(w & 0xffffu) + h1 * __uint_as_float(w & 0xffff0000u);
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t w = q == 0 ? bv[e].x : q == 1 ? bv[e].y : q == 2 ? bv[e].z : bv[e].w;
+                            low[e] += h0 * bf16_to_f32(w & 0xffffu) + h1 * __uint_as_float(w & 0xffff0000u);
+                        }
+                    }
                 }
             }
         }
-    }
-    float v[4];
-    sum_parts(parts, M * N, split, m * N + n, v);
+        float v[4];
+        sum_parts(parts, M * N, split, m * N + n, v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += low[e];
-    *reinterpret_cast<uint2*>(c + m * N + n) = pack4_bf16(v);
+        for (int e = 0; e < 4; ++e) v[e] += low[e];
+        const int64_t to = lr.order ? lr.order[m] : m;
+        *reinterpret_cast<uint2*>(c + to * N + n) = pack4_bf16(v);
+    }
 }
 
 // One row a workgroup, with its factor and (dr given) dr[row] = x . (the row without it).
@@ -413,15 +443,20 @@ bf16_join_rows_kernel(const float* __restrict__ parts, int64_t M, int64_t N, int
     if (threadIdx.x == 0) dr[row] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
 }
 
-__global__ void __launch_bounds__(256)
-scale_rows_kernel(const uint16_t* __restrict__ x, const float* __restrict__ r, int64_t M, int C8,
-                  uint16_t* __restrict__ out) {
-    // rows by grid, a row's 16-byte pieces by thread
-    for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
-        const float sc = r[row];
-        for (int c = threadIdx.x; c < C8; c += 256) {
-            const int64_t i = row * C8 + c;
-            const uint4 v = *reinterpret_cast<const uint4*>(x + i * 8);
+// Rows block, block + blocks, .. of out = bf16(r[row] x), a row's 16-byte pieces by thread.
+struct ScaleRows {
+    const uint16_t* x;
+    const float* r;
+    int64_t M;
+    int C8;                // row length in eights
+    uint16_t* out;
+};
+__device__ __forceinline__ void scale_rows(const ScaleRows& s, int block, int blocks) {
+    for (int64_t row = block; row < s.M; row += blocks) {
+        const float sc = s.r[row];
+        for (int c = threadIdx.x; c < s.C8; c += 256) {
+            const int64_t i = row * s.C8 + c;
+            const uint4 v = *reinterpret_cast<const uint4*>(s.x + i * 8);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             float f[8];
 #pragma unroll
@@ -429,8 +464,48 @@ scale_rows_kernel(const uint16_t* __restrict__ x, const float* __restrict__ r, i
                 f[2 * e] = bf16_to_f32(w[e] & 0xffffu) * sc;
                 f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u) * sc;
             }
-            *reinterpret_cast<uint4*>(out + i * 8) = pack8(f);
+            *reinterpret_cast<uint4*>(s.out + i * 8) = pack8(f);
         }
+    }
+}
+__global__ void __launch_bounds__(256)
+scale_rows_kernel(ScaleRows s) {
+    scale_rows(s, (int)blockIdx.x, (int)gridDim.x);
+}
+
+// Gradients' work that does not depend on each other, in one launch: the data gradient's
+// tiles (all, or what the large kernel left), the weight gradient's, the scaled copy of an
+// operand, dr of an earlier launch's partial sums.  A small call's workgroups fill the GPU
+// together, and a launch costs 2 to 3 us on the host as on the GPU.
+struct GradJobs {
+    SmallArgs d, w;
+    ScaleRows s;
+    const float* drp;
+    float* dr;
+    int64_t dr_rows;
+    int dr_parts;
+    int nd, nw, ns, nr;    // workgroups of each (nd, nw multiples of 128)
+};
+template <int MB>
+__global__ void __launch_bounds__(256, 2)
+bf16_grad_kernel(GradJobs j) {
+    union Smem {
+        uint8_t d[2][small_stage(MB)], w[2][small_stage(2)];
+    };
+    __shared__ __attribute__((aligned(16))) Smem sm;
+    int b = (int)blockIdx.x;
+    if (b < j.nd) return small_tile<Bf16Form::kDataGrad, MB>(j.d, b, sm.d);
+    b -= j.nd;
+    if (b < j.nw) return small_tile<Bf16Form::kWeightGrad, 2>(j.w, b, sm.w);
+    b -= j.nw;
+    if (b < j.ns) return scale_rows(j.s, b, j.ns);
+    b -= j.ns;
+    const int64_t row = (int64_t)b * 256 + threadIdx.x;
+    if (row < j.dr_rows) {
+        float sum = 0.f;
+#pragma unroll 16
+        for (int i = 0; i < j.dr_parts; ++i) sum += j.drp[i * j.dr_rows + row];
+        j.dr[row] = sum;
     }
 }
 
@@ -538,73 +613,112 @@ int64_t bf16_product_tiles(const Bf16Problem& p) {
 
 int64_t bf16_dr_parts(int64_t N) { return cdiv(N, 64); }
 
-hipError_t launch_bf16_product(const Bf16Problem& p, hipStream_t st) {
-    const Plan q = plan_of(p);
-    if (q.kind == kLarge) {
-        const bool tail = p.form != Bf16Form::kWeightGrad;
-        hipError_t e = launch_bf16_large(p, tail, st);
-        if (e != hipSuccess) return e;
-        if (tail) {
-            const SmallArgs t{p, 1, true, bf16_large_grid()};
-            const dim3 tg((4 * kTailMost + 127) / 128 * 128), tb(256);
-            if (p.form == Bf16Form::kForward)
-                hipLaunchKernelGGL((bf16_small_kernel<Bf16Form::kForward, 2>), tg, tb, 0, st, t);
-            else
-                hipLaunchKernelGGL((bf16_small_kernel<Bf16Form::kDataGrad, 2>), tg, tb, 0, st, t);
-            e = hipGetLastError();
-            if (e != hipSuccess) return e;
-        }
-        if (p.drp) return launch_dr_reduce(p.drp, p.M, bf16_dr_parts(p.N), p.dr, st);
-        return hipSuccess;
-    }
-    SmallArgs a{p, q.split, false, 0};
-    if (p.form == Bf16Form::kForward && p.M <= kLoraFewRows)
-        return launch_lora_few(p.A, p.M, p.K, p.B, p.N, p.lr, static_cast<uint16_t*>(p.C), st);
-    // The adapters' part in the tiles shares each adapter's b among up to 32 rows, in the
-    // join every row reads its own.
-    const bool join_lr = p.form == Bf16Form::kForward && a.split > 1 && p.M * p.N * p.lr.r <= (int64_t)1 << 25;
-    a.lr_here = !join_lr;
-    const int64_t grid = small_grid(p, q);
-    if (grid == 0) return hipSuccess;
-    const dim3 gd((unsigned)grid), bd(256);
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, gd, bd, 0, st, a); };
-    const bool small = q.kind == kSmall;
-    switch (p.form) {
-        case Bf16Form::kForward:
-            small ? go(bf16_small_kernel<Bf16Form::kForward, 1>) : go(bf16_small_kernel<Bf16Form::kForward, 2>);
-            break;
-        case Bf16Form::kDataGrad:
-            small ? go(bf16_small_kernel<Bf16Form::kDataGrad, 1>) : go(bf16_small_kernel<Bf16Form::kDataGrad, 2>);
-            break;
-        default:
-            go(bf16_small_kernel<Bf16Form::kWeightGrad, 2>);
-    }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (a.split > 1) {
-        if (join_lr) {
-            hipLaunchKernelGGL(bf16_join_adapters_kernel, dim3((unsigned)cdiv(p.N, 1024), (unsigned)p.M), bd, 0, st,
-                               p.parts, p.M, p.N, a.split, p.lr, static_cast<uint16_t*>(p.C));
-        } else if (p.rscale) {
-            hipLaunchKernelGGL(bf16_join_rows_kernel, dim3((unsigned)p.M), bd, 0, st, p.parts, p.M, p.N, a.split,
-                               p.rscale, p.drx, static_cast<uint16_t*>(p.C), p.dr);
-        } else {
-            const int64_t all = (p.form == Bf16Form::kWeightGrad ? (int64_t)p.G * p.M : p.rows) * p.N;
-            hipLaunchKernelGGL(bf16_join_kernel, dim3((unsigned)cdiv(all, 1024)), bd, 0, st, p.parts, all, a.split,
-                               p.C, p.c_f32, p.c_add);
-        }
-        return hipGetLastError();
-    }
-    if (p.drp) return launch_dr_reduce(p.drp, p.M, bf16_dr_parts(p.N), p.dr, st);
-    return hipSuccess;
+namespace {
+
+// Workgroups of the middle tiles that take what the large kernel left.
+constexpr int kRestGrid = (4 * kTailMost + 127) / 128 * 128;
+
+hipError_t join_shares(const Bf16Problem& p, int split, hipStream_t st) {
+    const int64_t all = (p.form == Bf16Form::kWeightGrad ? (int64_t)p.G * p.M : p.rows) * p.N;
+    if (p.rscale)
+        hipLaunchKernelGGL(bf16_join_rows_kernel, dim3((unsigned)p.M), dim3(256), 0, st, p.parts, p.M, p.N, split,
+                           p.rscale, p.drx, static_cast<uint16_t*>(p.C), p.dr);
+    else
+        hipLaunchKernelGGL(bf16_join_kernel, dim3((unsigned)cdiv(all, 1024)), dim3(256), 0, st, p.parts, all, split,
+                           p.C, p.c_f32, p.c_add);
+    return hipGetLastError();
 }
 
-hipError_t launch_scale_rows(const uint16_t* x, const float* r, int64_t M, int64_t C, uint16_t* out,
-                             hipStream_t s) {
-    if (M == 0) return hipSuccess;
-    hipLaunchKernelGGL(scale_rows_kernel, dim3((unsigned)(M < 65536 ? M : 65536)), dim3(256), 0, s, x, r, M,
-                       (int)(C / 8), out);
+hipError_t launch_jobs(GradJobs& j, bool small_d, hipStream_t st) {
+    const int grid = j.nd + j.nw + j.ns + j.nr;
+    if (grid == 0) return hipSuccess;
+    if (small_d) hipLaunchKernelGGL(bf16_grad_kernel<1>, dim3(grid), dim3(256), 0, st, j);
+    else hipLaunchKernelGGL(bf16_grad_kernel<2>, dim3(grid), dim3(256), 0, st, j);
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_lora_product(const Bf16Problem& p, hipStream_t st) {
+    const Plan q = plan_of(p);
+    const dim3 bd(256);
+    if (q.kind == kLarge) {
+        const hipError_t e = launch_bf16_large(p, true, st);
+        if (e != hipSuccess) return e;
+        const SmallArgs rest{p, 1, true, bf16_large_grid()};
+        hipLaunchKernelGGL(bf16_forward_kernel<2>, dim3(kRestGrid), bd, 0, st, rest);
+        return hipGetLastError();
+    }
+    // The adapters' part in the tiles shares each adapter's b among up to 32 rows, in the
+    // join every row reads its own.
+    const bool join_lr = q.split > 1 && p.M * p.N * p.lr.r <= (int64_t)1 << 25;
+    const SmallArgs a{p, q.split, !join_lr, 0};
+    const dim3 gd((unsigned)small_grid(p, q));
+    if (q.kind == kSmall) hipLaunchKernelGGL(bf16_forward_kernel<1>, gd, bd, 0, st, a);
+    else hipLaunchKernelGGL(bf16_forward_kernel<2>, gd, bd, 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || q.split == 1) return e;
+    const dim3 gj((unsigned)cdiv(p.N, 1024), (unsigned)(p.M < 65535 ? p.M : 65535));
+    auto join = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, gj, bd, 0, st, p.parts, p.M, p.N, q.split, p.lr, static_cast<uint16_t*>(p.C));
+    };
+    join_lr ? join(bf16_join_adapters_kernel<true>) : join(bf16_join_adapters_kernel<false>);
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_grads(const Bf16Problem* d, const Bf16Problem* w, const uint16_t* scale_x,
+                               const float* scale_r, int64_t scale_cols, uint16_t* scaled, hipStream_t st) {
+    const Plan pd = d ? plan_of(*d) : Plan{kLarge, 1}, pw = w ? plan_of(*w) : Plan{kLarge, 1};
+    const bool d_tiles = d && pd.kind != kLarge, w_tiles = w && pw.kind != kLarge;
+    bool dr_left = d && d->drp && !(d_tiles && pd.split > 1);    // (the rows' join makes dr)
+    const ScaleRows sr{scale_x, scale_r, w ? w->rows : 0, (int)(scale_cols / 8), scaled};
+    // a scaled copy goes with the data gradient's tiles if it is small, else before them
+    const bool scale_with = scaled && d_tiles && sr.M * scale_cols <= (int64_t)1 << 22;
+    hipError_t e = hipSuccess;
+    if (scaled && !scale_with) {
+        hipLaunchKernelGGL(scale_rows_kernel, dim3((unsigned)(sr.M < 65536 ? sr.M : 65536)), dim3(256), 0, st, sr);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (d && !d_tiles) {
+        e = launch_bf16_large(*d, true, st);
+        if (e != hipSuccess) return e;
+    }
+    GradJobs j{};
+    if (d) {
+        j.d = d_tiles ? SmallArgs{*d, pd.split, false, 0} : SmallArgs{*d, 1, false, bf16_large_grid()};
+        j.nd = d_tiles ? (int)small_grid(*d, pd) : kRestGrid;
+    }
+    auto with_w = [&] {
+        j.w = SmallArgs{*w, pw.split, false, 0};
+        j.nw = (int)small_grid(*w, pw);
+    };
+    const bool w_now = w_tiles && !scale_with;
+    if (w_now) with_w();
+    if (scale_with) {
+        j.s = sr;
+        j.ns = (int)(sr.M < 512 ? sr.M : 512);
+    }
+    e = launch_jobs(j, d_tiles && pd.kind == kSmall, st);
+    if (e == hipSuccess && d_tiles && pd.split > 1) e = join_shares(*d, pd.split, st);
+    if (e != hipSuccess) return e;
+    GradJobs k{};
+    if (w_tiles && !w_now) {
+        j = k;
+        with_w();
+        k = j;
+    }
+    if (dr_left) {
+        k.drp = d->drp;
+        k.dr = d->dr;
+        k.dr_rows = d->M;
+        k.dr_parts = (int)bf16_dr_parts(d->N);
+        k.nr = (int)cdiv(d->M, 256);
+    }
+    e = launch_jobs(k, false, st);
+    if (e == hipSuccess && w && !w_tiles) e = launch_bf16_large(*w, false, st);
+    if (e == hipSuccess && w_tiles && pw.split > 1) e = join_shares(*w, pw.split, st);
+    return e;
 }
 
 }  // namespace mx

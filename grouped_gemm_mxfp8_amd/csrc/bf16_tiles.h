@@ -161,10 +161,12 @@ __device__ __forceinline__ int line_chunk(int lane) {
 
 // 32 rows x 64 columns (two accumulators) as bf16 lines.  base: row 0, column 0
 // (wave-uniform), ldb: bytes between rows; rows and cols: how many of them exist
-// (cols a multiple of 8).  sc: the factor of row lane & 31.
-template <bool SCALED>
+// (cols a multiple of 8).  sc: the factor of row lane & 31.  MAPPED: base is row 0 of the
+// matrix and at[t] the row that store t's row 8 t + (lane & 7) belongs at.
+template <bool SCALED, bool MAPPED = false>
 __device__ __forceinline__ void store_bf16_32x64(const v16f& a0, const v16f& a1, float sc, uint8_t* base,
-                                                 uint32_t ldb, int rows, int cols, int lane) {
+                                                 uint32_t ldb, int rows, int cols, int lane,
+                                                 const int (&at)[4] = {0, 0, 0, 0}) {
     uint32_t x[4][4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -191,7 +193,19 @@ __device__ __forceinline__ void store_bf16_32x64(const v16f& a0, const v16f& a1,
 #pragma unroll
         for (int t = 0; t < 4; ++t)
             if (8 * t + r8 < rows)
-                store_nt(base + (int64_t)(8 * t) * ldb + off, make_uint4(x[t][0], x[t][1], x[t][2], x[t][3]));
+                store_nt(MAPPED ? base + (int64_t)at[t] * ldb + (uint32_t)chunk * 16u
+                                : base + (int64_t)(8 * t) * ldb + off,
+                         make_uint4(x[t][0], x[t][1], x[t][2], x[t][3]));
+    }
+}
+
+// Where the rows of a block's four stores belong (its row 0 is row r0): order's, or as
+// they are.
+__device__ __forceinline__ void line_rows(int (&at)[4], const int32_t* order, int64_t r0, int rows, int lane) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int r = 8 * t + (lane & 7);
+        at[t] = order ? (r < rows ? order[r0 + r] : 0) : (int)(r0 + r);
     }
 }
 

@@ -236,7 +236,14 @@ struct LowRank {
     const uint16_t* b;       // [L][N][r]
     const int32_t* id;       // [M]
     int r, L;
+    const int32_t* order;    // rows m of A, of h and of id belong at row order[m] of x and C
+                             // (A is then x itself, M K < 2^30), or null: as they are
 };
+// Whether a call's rows are put in the order of their adapters: order and id come from
+// launch_lora_sort.
+bool lora_sorts(int64_t M, int64_t K, int L);
+hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int L, int32_t* order, int32_t* sorted_ids,
+                            hipStream_t s);
 struct Bf16Problem {
     Bf16Form form;
     const int64_t* offs;     // [G + 1] groups of rows (kForward: null, one group of M)
@@ -264,19 +271,25 @@ int64_t bf16_dr_parts(int64_t N);
 // whole_rounds; the rest is then the middle tiles'), bf16_large_grid() workgroups.
 int bf16_large_grid();
 hipError_t launch_bf16_large(const Bf16Problem& p, bool tail, hipStream_t s);
-hipError_t launch_bf16_product(const Bf16Problem& p, hipStream_t s);
-// out = bf16(r[row] x), [M][C], C % 8 == 0.
-hipError_t launch_scale_rows(const uint16_t* x, const float* r, int64_t M, int64_t C, uint16_t* out,
-                             hipStream_t s);
+// kForward with its adapters.
+hipError_t launch_lora_product(const Bf16Problem& p, hipStream_t s);
+// The data gradient d and the weight gradient w (either may be null).  scaled (or null):
+// an operand of w that is made first, bf16(scale_r[row] scale_x), [w->rows][scale_cols],
+// scale_cols % 8 == 0.  Both have parts of their own.
+hipError_t launch_linear_grads(const Bf16Problem* d, const Bf16Problem* w, const uint16_t* scale_x,
+                               const float* scale_r, int64_t scale_cols, uint16_t* scaled, hipStream_t s);
 // h [M][2 r] = scale[id] x a[id]^T as high and low bf16 parts (rows without an
-// adapter are not written); a [L][r][K], K % 32 == 0, r % 8 == 0.
+// adapter are not written); a [L][r][K], K % 32 == 0, r % 8 == 0.  order: row m is row
+// order[m] of x, or null.
 hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, const uint16_t* a,
-                            const int32_t* id, const float* scale, int L, int r, uint16_t* h,
-                            hipStream_t s);
-// y [M][N] = x w^T + the adapters' part for up to kLoraFewRows rows, N % 16 == 0.
+                            const int32_t* id, const int32_t* order, const float* scale, int L, int r,
+                            uint16_t* h, hipStream_t s);
+// y [M][N] = x w^T + the adapters' part for up to kLoraFewRows rows, N % 16 == 0.  Where
+// lora_fuses, h is made here of a and scale (lr.h is then not read).
 constexpr int kLoraFewRows = 16;
+bool lora_fuses(int64_t M, int r);
 hipError_t launch_lora_few(const uint16_t* x, int64_t M, int64_t K, const uint16_t* w, int64_t N, const LowRank& lr,
-                           uint16_t* y, hipStream_t s);
+                           const uint16_t* a, const float* scale, uint16_t* y, hipStream_t s);
 
 int device_cu_count();
 

@@ -200,15 +200,16 @@ mx_status grouped_linear_fwd(int32_t dtype, const void* x,
  *          MX_BWD_DW_ADD (with MX_BWD_DW_FP32): added to what dw holds, as gradients
  *          of several micro-batches are; experts with no rows keep theirs.
  *          Otherwise every value is written, zeros for experts with no rows.
- *   ws     grouped_linear_bwd_ws_bytes(..) bytes of scratch, 256-byte aligned, not
- *          shared with a call that may run at the same time.
+ *   ws     grouped_linear_bwd_ws_bytes(..) bytes of scratch (scaled: whether there are row
+ *          scales), 256-byte aligned, not shared with a call that may run at the same
+ *          time; may be NULL where that is 256, which means none.
  * K % 32 == 0 and N % 16 == 0, both up to 2^21 (MX_ERR_UNSUPPORTED otherwise); dy, x,
  * w, dx and dw 16-byte aligned; outputs and ws must not overlap inputs.  Nothing is
  * allocated.  With M == 0, dy, x and dx may have no storage (dw is written).
  */
 #define MX_BWD_DW_FP32 1u
 #define MX_BWD_DW_ADD 2u
-size_t grouped_linear_bwd_ws_bytes(int32_t E, int64_t M, int64_t N, int64_t K);
+size_t grouped_linear_bwd_ws_bytes(int32_t E, int64_t M, int64_t N, int64_t K, int32_t scaled);
 mx_status grouped_linear_bwd(const void* dy, const void* x, const int64_t* d_offsets, int32_t E,
                              int64_t M, const void* w, int64_t N, int64_t K,
                              const float* d_row_scale, void* dx, float* d_dr, void* dw,
@@ -231,7 +232,8 @@ mx_status grouped_linear_bwd(const void* dy, const void* x, const int64_t* d_off
  *   MX_LORA_MAX_RANK (MX_ERR_UNSUPPORTED otherwise); x, w, a, b and y 16-byte aligned;
  *   y and ws must not overlap inputs.  Nothing is allocated.
  *   ws     lora_linear_ws_bytes(..) bytes of scratch, 256-byte aligned, not shared with
- *          a call that may run at the same time.
+ *          a call that may run at the same time; may be NULL where that is 256, which
+ *          means none.
  * Adapters are trained as two GroupedLinears with rows sorted by adapter (a and b as w)
  * and their grouped_linear_bwd.
  */

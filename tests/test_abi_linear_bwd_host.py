@@ -49,7 +49,8 @@ def test_linear_bwd_refusals(mxlib, change, status, text):
     (dict(M=(1 << 31) - 1, N=1 << 21), UNSUPPORTED, "launch"),
     (dict(x=ODD), INVALID, "aligned"), (dict(w=ODD), INVALID, "aligned"), (dict(a=ODD), INVALID, "aligned"),
     (dict(b=ODD), INVALID, "aligned"), (dict(y=ODD), INVALID, "aligned"), (dict(ws=ODD), INVALID, "aligned"),
-    (dict(n=16), WORKSPACE, "needs"),
+    (dict(n=16), WORKSPACE, "needs"), (dict(n=256, M=2, r=24), WORKSPACE, "needs"),
+    (dict(ws=None, M=2, r=24), INVALID, "NULL ws"),
 ])
 def test_lora_refusals(mxlib, change, status, text):
     assert mxlib.lora_linear_fwd(*{**LORA, **change}.values(), None) == status
@@ -58,10 +59,13 @@ def test_lora_refusals(mxlib, change, status, text):
 
 def test_workspace_sizes(mxlib):
     for L in (mxlib,):
-        assert L.grouped_linear_bwd_ws_bytes(2, 0, 16, 32) > 0
-        assert L.grouped_linear_bwd_ws_bytes(2, 8, 24, 32) == 0
-        assert L.lora_linear_ws_bytes(0, 16, 32, 1, 8) > 0
+        assert L.grouped_linear_bwd_ws_bytes(2, 0, 16, 32, 0) == 256
+        assert L.grouped_linear_bwd_ws_bytes(2, 8, 24, 32, 1) == 0
+        assert L.lora_linear_ws_bytes(0, 16, 32, 1, 8) == 256
         assert L.lora_linear_ws_bytes(1, 16, 32, 1, 9) == 0
+    # 256 stands for no scratch at all, also where all of it would fit into 256 bytes
+    assert mxlib.lora_linear_ws_bytes(2, 16, 96, 2, 24) == 512
+    assert mxlib.lora_linear_ws_bytes(1, 4096, 4096, 8, 16) == 256
     # no rows: nothing to launch for an adapter linear
     assert mxlib.lora_linear_fwd(None, 0, 64, None, 64, None, None, 1, 8, None, None, None, None, 0, None) == 0
 

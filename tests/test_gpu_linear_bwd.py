@@ -92,7 +92,7 @@ LARGE = [
 @pytest.mark.parametrize("counts,N,K", SHAPES + LARGE)
 def test_against_fp64(dev, counts, N, K, scaled):
     dy, x, w, off, offd, r = make(counts, N, K, N + K, dev, scaled)
-    nws = gm.lib().grouped_linear_bwd_ws_bytes(len(counts), x.shape[0], N, K)
+    nws = gm.lib().grouped_linear_bwd_ws_bytes(len(counts), x.shape[0], N, K, scaled)
     ws = torch.full((nws,), 255, dtype=torch.uint8, device=dev)
     dx, dw, dr = gm.grouped_linear_bwd(dy, x, offd, w, row_scale=r, ws=ws)
     dx2, dw2, dr2 = gm.grouped_linear_bwd(dy, x, offd, w, row_scale=r, dw_dtype=torch.float32)
@@ -147,7 +147,7 @@ def test_only_what_is_asked_for_is_written(dev, counts, N, K):
     them, and outputs that are not asked for, stay as they were."""
     dy, x, w, off, offd, r = make(counts, N, K, 4, dev, True)
     M, E, L = x.shape[0], len(counts), gm.lib()
-    nws = L.grouped_linear_bwd_ws_bytes(E, M, N, K)
+    nws = L.grouped_linear_bwd_ws_bytes(E, M, N, K, 1)
     ws = torch.full((nws + 256,), 7, dtype=torch.uint8, device=dev)
     mark = 1234.0
     bufs = {"dx": torch.full((M * K + 4096,), mark, dtype=torch.bfloat16, device=dev),
@@ -198,7 +198,7 @@ def test_what_is_not_finite_stays_in_its_row_and_expert(dev, counts, N, K):
 @pytest.mark.parametrize("counts,N,K", [([33, 0, 60], 80, 96), ([900, 300], 784, 544)])
 def test_captured_and_replayed(dev, counts, N, K):
     dy, x, w, off, offd, r = make(counts, N, K, 11, dev, True)
-    ws = torch.empty(gm.lib().grouped_linear_bwd_ws_bytes(len(counts), x.shape[0], N, K), dtype=torch.uint8,
+    ws = torch.empty(gm.lib().grouped_linear_bwd_ws_bytes(len(counts), x.shape[0], N, K, 1), dtype=torch.uint8,
                      device=dev)
     buf = torch.zeros(w.shape, device=dev)
     gm.grouped_linear_bwd(dy, x, offd, w, row_scale=r, ws=ws)

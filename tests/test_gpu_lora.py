@@ -50,6 +50,9 @@ SHAPES = [
     (100, 1024, 336, 8, 200, "each"), (130, 32, 2064, 16, 4, "mixed"), (257, 704, 528, 56, 6, "mixed"),
     (300, 544, 256, 512, 2, "mixed"), (515, 416, 1040, 16, 3, 1), (1000, 288, 784, 24, 8, "mixed"),
     (1500, 608, 1296, 32, 4, "mixed"), (700, 96, 2320, 8, 40, "each"),
+    # sorted by adapter (eight rows an adapter on average), and the same unsorted
+    (257, 96, 144, 8, 32, "each"), (600, 160, 528, 16, 75, "each"), (600, 160, 528, 16, 76, "each"),
+    (1300, 1056, 272, 128, 3, "each"), (2049, 64, 2064, 24, 200, "each"),
     # enough tiles for the large kernel: whole rounds of 256 and what is left of them
     (4096, 64, 4096, 16, 3, "mixed"), (4200, 96, 4624, 24, 5, "mixed"), (5003, 288, 4112, 8, 70, "each"),
     (4400, 352, 4096, 64, 2, -1),
