@@ -785,7 +785,7 @@ mx_status lora_linear_fwd(const void* x, int64_t M, int64_t K, const void* w, in
     const uint16_t* const x16 = static_cast<const uint16_t*>(x);
     const uint16_t *const a16 = static_cast<const uint16_t*>(a), *const w16 = static_cast<const uint16_t*>(w);
     mx::LowRank lr{h, static_cast<const uint16_t*>(b), d_ids, r, L, nullptr};
-    const double flops = 2.0 * M * N * (K + r);
+    const double flops = 2.0 * M * N * (K + r);    // (and 2 M r K of h)
     mx_status ls;
     if (mx::lora_sorts(M, K, L)) {
         int32_t *const to = reinterpret_cast<int32_t*>(base + W.order), *const sid = reinterpret_cast<int32_t*>(base + W.ids);
@@ -796,26 +796,28 @@ mx_status lora_linear_fwd(const void* x, int64_t M, int64_t K, const void* w, in
         lr.id = sid;
         lr.order = to;
     }
-    if (M > mx::kLoraFewRows || !mx::lora_fuses(M, r)) {
-        ls = launched(timed("lora_down", 2.0 * M * r * K, MX_WORK_FLOP, s,
-                            [&] { return mx::launch_lora_down(x16, M, K, a16, lr.id, lr.order, d_scale, L, r, h, s); }),
-                      "lora_down");
-        if (ls != MX_OK) return ls;
-    }
-    if (M <= mx::kLoraFewRows)
+    const mx::LoraDown down{x16, M, K, a16, lr.id, lr.order, d_scale, L, r, h};
+    if (M <= mx::kLoraFewRows) {
+        if (!mx::lora_fuses(M, r)) {
+            ls = launched(timed("lora_down", 2.0 * M * r * K, MX_WORK_FLOP, s,
+                                [&] { return mx::launch_lora_down(down, s); }),
+                          "lora_down");
+            if (ls != MX_OK) return ls;
+        }
         return launched(timed("lora_few", flops, MX_WORK_FLOP, s,
                               [&] {
                                   return mx::launch_lora_few(x16, M, K, w16, N, lr, a16, d_scale,
                                                              static_cast<uint16_t*>(y), s);
                               }),
                         "lora_few");
+    }
     mx::Bf16Problem p = lora_problem(M, N, K);
     p.A = x16;
     p.B = w16;
     p.C = y;
     p.lr = lr;
     p.parts = reinterpret_cast<float*>(base + W.parts);
-    return launched(timed("lora_linear", flops, MX_WORK_FLOP, s, [&] { return mx::launch_lora_product(p, s); }),
+    return launched(timed("lora_linear", flops, MX_WORK_FLOP, s, [&] { return mx::launch_lora_product(p, down, s); }),
                     "lora_linear");
 }
 

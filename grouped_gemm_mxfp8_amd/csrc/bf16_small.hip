@@ -3,19 +3,21 @@
 // data and weight gradients of GroupedLinear and the adapter linear.
 //
 // One workgroup of four waves per tile and share of K; each wave owns 32 RB x 64 (RB x 2
-// accumulators of the 32x32x16 MFMA).  K goes in steps of 64 through two LDS stages
-// filled by direct loads, so two workgroups share a CU.  As in the large kernel a step's
-// fragments are in registers before it begins and its stage is refilled during it, and
-// the next step's are read into the registers that its second half's MFMAs free (read
-// where the compiler puts them, a step of a workgroup alone on its CU took 1800 cycles
-// for 512 of MFMAs).  Where the tiles alone leave CUs idle, K is cut into `split` shares,
-// whose fp32 sums go to memory and are added in order by a second launch: one order of
-// every sum, no atomics.
+// accumulators of the 32x32x16 MFMA).  K goes in steps of 64 through LDS stages filled by
+// direct loads.  A step's fragments are read into registers all along the step before it,
+// so one barrier a step is enough: behind it the next step's stage has landed and this
+// step's, already read, is refilled.  (With the reads in the half of a step that follows
+// a second barrier, as registers allow the large kernel, that half is bound by the LDS:
+// 6 to 10 % slower here.)  Two stages let two workgroups share a CU and hide each other's
+// waits; a launch of at most one workgroup a CU takes three (256 tiles of 64 x 128, K =
+// 4096: 31 us, with two stages 40).  Where the tiles alone leave CUs idle, K is cut into
+// `split` shares, whose fp32 sums go to memory and are added in order by a second launch:
+// one order of every sum, no atomics.
 //
 // LDS orders (64 banks of 4 bytes): along K, chunk c of line n is stored at
 // c ^ (n >> 1 & 7); across K, the 64-byte quarter of a 256-byte row at quarter ^ (k & 3),
 // so that the rows that one transposing read takes lie on different banks.
-#include "bf16_tiles.h"
+#include "lora_down.h"
 
 namespace mx {
 namespace {
@@ -23,11 +25,6 @@ namespace {
 // MB: 32-row blocks of a wave (1: tiles of 64 x 128, 2: of 128 x 128).
 constexpr int SM_N = 128, SM_K = 64, SM_B = SM_N * 128;
 constexpr int small_m(int MB) { return 64 * MB; }
-
-// The steps' MFMAs in order: slot t is row block t / 8, sixteen t / 2 % 4 of K, column
-// block t % 2 (one that follows the one whose result it adds to would wait).  Loads go
-// one to a slot from the first half's second quarter on.
-constexpr int first_loads(int MB) { return MB == 1 ? 2 : 4; }
 
 struct SmallArgs {
     Bf16Problem p;
@@ -46,12 +43,13 @@ __device__ __forceinline__ v4i across_rsrc(const uint16_t* p, int64_t k0, int64_
 constexpr int small_stage(int MB) { return small_m(MB) * 128 + SM_B; }
 
 // What workgroup `block` (of a multiple of 128) of a product's does.
-template <Bf16Form F, int MB>
+template <Bf16Form F, int MB, int ST>
 __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
-                                           uint8_t (&sm)[2][small_stage(MB)]) {
+                                           uint8_t (&sm)[ST][small_stage(MB)]) {
     constexpr int SM_M = small_m(MB), SM_A = SM_M * 128, SM_STAGE = small_stage(MB);
     constexpr int SM_LOADS = 2 * MB + 4;                  // per wave and step, of A and B
-    constexpr int SLOTS = 8 * MB, FIRST = first_loads(MB);
+    constexpr int SLOTS = 8 * MB, READS = 4 * (MB + 2);   // of a step: MFMAs, fragments
+    constexpr int WAIT = 2 * MB;                          // MFMAs before its barrier
     constexpr bool kA = F != Bf16Form::kWeightGrad;       // A lies along K
     constexpr bool kB = F == Bf16Form::kForward;          // B lies along K
     constexpr bool kRows = F != Bf16Form::kWeightGrad;    // groups own rows of C
@@ -209,56 +207,67 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
     v16f acc[MB][2];
 #pragma unroll
     for (int i = 0; i < MB; ++i) acc[i][0] = acc[i][1] = zero16();
-    bf16x8 af[MB][4], bf[2][4];
-    auto step = [&](int ks) {
-        const int cur = (ks - k_beg) & 1;
-        const uint8_t* const nxt = sm[cur ^ 1];
-        const Rsrc r = rsrc_of(ks + 2);
+    // A step's fragments are read during the one before it, all along it, so its stage is
+    // free when it begins.
+    struct Frags {
+        bf16x8 a[MB][4], b[2][4];
+    };
+    auto read = [&](auto nc, Frags& f, const uint8_t* st) {      // in the order of their use
+        constexpr int n = decltype(nc)::value, kk = n / (MB + 2), w = n % (MB + 2);
+        if constexpr (w < 2) f.b[w][kk] = frag_b(st, w, kk);
+        else f.a[w - 2][kk] = frag_a(st, w - 2, kk);
+    };
+    auto step = [&](int ks, Frags& cur, Frags& nxt) {
+        const int st = (ks - k_beg) % ST;
+        const uint8_t* const from = sm[(ks + 1 - k_beg) % ST];
+        const Rsrc r = rsrc_of(ks + ST);
         static_for<SLOTS>([&](auto tc) {
-            constexpr int t = decltype(tc)::value, i = t / 8, kk = t / 2 % 4, j = t % 2, q = t - SLOTS / 2;
-            if constexpr (t == SLOTS / 4) lds_barrier();      // every wave holds this step's fragments
-            if constexpr (q == 0) {
-                wait_vm<FIRST>();                             // this wave's loads of step ks + 1
-                lds_barrier();                                // and everybody's have landed
+            constexpr int t = decltype(tc)::value, kk = t / (2 * MB), i = t / 2 % MB, j = t % 2;
+            constexpr int at = t - WAIT;          // of the slots behind the barrier
+            if constexpr (at == 0) {
+                wait_vm<(ST - 2) * SM_LOADS>();   // this wave's loads of step ks + 1 have landed
+                lds_barrier();                    // and everybody's, and this step's stage is read
             }
-            acc[i][j] = mfma_bf16(bf[j][kk], af[i][kk], acc[i][j]);
+            acc[i][j] = mfma_bf16(cur.b[j][kk], cur.a[i][kk], acc[i][j]);
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (t >= SLOTS / 4 && t - SLOTS / 4 < SM_LOADS)
-                dma(std::integral_constant<int, t - SLOTS / 4>{}, r, cur);
-            if constexpr (MB == 2 && q >= 0 && q < 4) af[0][q] = frag_a(nxt, 0, q);
-            if constexpr (MB == 1 && q >= 0 && q < 2) {
-                af[0][q] = frag_a(nxt, 0, q);
-                bf[0][q] = frag_b(nxt, 0, q);
-                bf[1][q] = frag_b(nxt, 1, q);
-            }
-            if constexpr (q >= 0 && j == 1) {                 // this sixteen is done with
-                af[MB - 1][kk] = frag_a(nxt, MB - 1, kk);
-                bf[0][kk] = frag_b(nxt, 0, kk);
-                bf[1][kk] = frag_b(nxt, 1, kk);
+            if constexpr (at >= 0) {
+                constexpr int per = (READS + SLOTS - WAIT - 2) / (SLOTS - WAIT - 1);   // none in the last
+                static_for<per>([&](auto uc) {
+                    constexpr int n = at * per + decltype(uc)::value;
+                    if constexpr (n < READS) read(std::integral_constant<int, n>{}, nxt, from);
+                });
+                constexpr int lper = (SM_LOADS + SLOTS - WAIT - 1) / (SLOTS - WAIT);
+                static_for<lper>([&](auto uc) {
+                    constexpr int n = at * lper + decltype(uc)::value;
+                    if constexpr (n < SM_LOADS) dma(std::integral_constant<int, n>{}, r, st);
+                });
             }
             __builtin_amdgcn_sched_barrier(0);
         });
     };
+    Frags f0, f1;
     {
         const Rsrc r0 = rsrc_of(k_beg);
         static_for<SM_LOADS>([&](auto uc) { dma(uc, r0, 0); });
         if (k_beg + 1 < k_end) {
-            const Rsrc r1 = rsrc_of(k_beg + 1);
-            static_for<SM_LOADS>([&](auto uc) { dma(uc, r1, 1); });
-            wait_vm<SM_LOADS>();
+            static_for<ST - 1>([&](auto ic) {
+                constexpr int i = decltype(ic)::value + 1;
+                const Rsrc r1 = rsrc_of(k_beg + i);
+                static_for<SM_LOADS>([&](auto uc) { dma(uc, r1, i); });
+            });
+            wait_vm<(ST - 1) * SM_LOADS>();
         } else {
             wait_vm<0>();
         }
         lds_barrier();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-            for (int i = 0; i < MB; ++i) af[i][kk] = frag_a(sm[0], i, kk);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) bf[j][kk] = frag_b(sm[0], j, kk);
-        }
+        static_for<READS>([&](auto nc) { read(nc, f0, sm[0]); });
     }
-    for (int ks = k_beg; ks < k_end; ++ks) step(ks);
+    int ks = k_beg;
+    for (; ks + 2 <= k_end; ks += 2) {
+        step(ks, f0, f1);
+        step(ks + 1, f1, f0);
+    }
+    if (ks < k_end) step(ks, f0, f1);
     wait_vm<0>();          // no load may still be landing in LDS when the workgroup ends
 
     // ---- output: the wave's blocks of 32 x 64 ----
@@ -320,11 +329,26 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
     });
 }
 
-template <int MB>
-__global__ void __launch_bounds__(256, 2)
+template <int MB, int ST>
+__global__ void __launch_bounds__(256, ST == 2 ? 2 : 1)
 bf16_forward_kernel(SmallArgs s) {
-    __shared__ __attribute__((aligned(16))) uint8_t sm[2][small_stage(MB)];
-    small_tile<Bf16Form::kForward, MB>(s, (int)blockIdx.x, sm);
+    __shared__ __attribute__((aligned(16))) uint8_t sm[ST][small_stage(MB)];
+    small_tile<Bf16Form::kForward, MB, ST>(s, (int)blockIdx.x, sm);
+}
+
+// The same with the adapters' down projection in the workgroups from `tiles` on, for calls
+// whose join adds the adapters' part.
+template <int MB, int ST>
+__global__ void __launch_bounds__(256, ST == 2 ? 2 : 1)
+bf16_forward_down_kernel(SmallArgs s, LoraDown d, int tiles) {
+    union Smem {
+        uint8_t tile[ST][small_stage(MB)];
+        v4f sum[4][1][64];
+    };
+    __shared__ __attribute__((aligned(16))) Smem sm;
+    const int b = (int)blockIdx.x - tiles, ranks = d.r / 4;
+    if (b < 0) return small_tile<Bf16Form::kForward, MB, ST>(s, (int)blockIdx.x, sm.tile);
+    lora_down<4, 1, true>(d, b / (4 * ranks), b / 4 % ranks, b % 4, sm.sum);
 }
 
 // ---- sums of the shares ------------------------------------------------------------
@@ -486,18 +510,21 @@ struct GradJobs {
     int dr_parts;
     int nd, nw, ns, nr;    // workgroups of each (nd, nw multiples of 128)
 };
-template <int MB>
-__global__ void __launch_bounds__(256, 2)
+// MB and ST are the data gradient's.
+template <int MB, int ST>
+__global__ void __launch_bounds__(256, ST == 2 ? 2 : 1)
 bf16_grad_kernel(GradJobs j) {
     union Smem {
-        uint8_t d[2][small_stage(MB)], w[2][small_stage(2)];
+        uint8_t d[ST][small_stage(MB)], w[ST == 2 ? 2 : 1][small_stage(2)];
     };
     __shared__ __attribute__((aligned(16))) Smem sm;
     int b = (int)blockIdx.x;
-    if (b < j.nd) return small_tile<Bf16Form::kDataGrad, MB>(j.d, b, sm.d);
+    if (b < j.nd) return small_tile<Bf16Form::kDataGrad, MB, ST>(j.d, b, sm.d);
     b -= j.nd;
-    if (b < j.nw) return small_tile<Bf16Form::kWeightGrad, 2>(j.w, b, sm.w);
-    b -= j.nw;
+    if constexpr (ST == 2) {                       // (a launch with both has no need of three)
+        if (b < j.nw) return small_tile<Bf16Form::kWeightGrad, 2, 2>(j.w, b, sm.w);
+        b -= j.nw;
+    }
     if (b < j.ns) return scale_rows(j.s, b, j.ns);
     b -= j.ns;
     const int64_t row = (int64_t)b * 256 + threadIdx.x;
@@ -525,6 +552,7 @@ enum Kind { kLarge = 0, kSmall = 1, kMiddle = 2 };     // (kSmall, kMiddle: also
 struct Plan {
     Kind kind;
     int split;
+    bool alone = false;    // at most one workgroup a CU
 };
 
 // Rows of groups are on the device: groups are taken as equal here.
@@ -532,8 +560,8 @@ struct Plan {
 // Products whose groups own rows: the fastest by a model of their times, in us, its
 // numbers measured at K x N of 4096 x 4096, 1408 x 2064, 4096 x 14336 and 1024 x 1024
 // with 17 to 8192 rows, and at 1 to 64 experts with 4 to 4096 rows each.  A tile's step
-// of 64 in K takes a CU 0.45 (small) or 0.75 (middle) for a workgroup alone, 0.35 or 0.52
-// a workgroup when it has several, and 1.6 (large, four middle ones' work); starting and
+// of 64 in K takes a CU 0.4 (small) or 0.56 (middle) for a workgroup alone, 0.34 or 0.52 a
+// workgroup when it has several, and 1.6 (large, four middle ones' work); starting and
 // storing take 6, a large round 12 in all; adding the shares of a split K takes 4.5 and
 // the time its bytes need.  A last round of large tiles goes to middle ones where
 // whole_rounds says so.
@@ -544,7 +572,7 @@ Plan plan_rows(const Bf16Problem& p) {
     auto tiles = [&](int bm, int bn) { return (double)(groups * cdiv(rows, bm) * cdiv(p.N, bn)); };
     auto tile_us = [&](Kind k, double units, double steps) {
         const double each = units / 256;
-        return each <= 1 ? steps * (k == kSmall ? 0.45 : 0.75) : steps * (k == kSmall ? 0.35 : 0.52) * (each < 2 ? 2 : each);
+        return each <= 1 ? steps * (k == kSmall ? 0.4 : 0.56) : steps * (k == kSmall ? 0.34 : 0.52) * (each < 2 ? 2 : each);
     };
     Plan best{kSmall, 1};
     double least = 1e30;
@@ -555,21 +583,21 @@ Plan plan_rows(const Bf16Problem& p) {
             if (split > 1) us += 4.5 + 8e-6 * split * p.rows * p.N / 3;
             if (us < least) {
                 least = us;
-                best = Plan{k, split};
+                best = Plan{k, split, small_tiles(p, k) * split <= 256};
             }
         }
         if (t > 1024 && 6 + tile_us(k, t, nk) < least) {
             least = 6 + tile_us(k, t, nk);
-            best = Plan{k, 1};
+            best = Plan{k, 1, false};
         }
     }
     const double t = tiles(256, 256);
     if (t < 1e9) {
         const int whole = whole_rounds((int)t, 256), rest = (int)t - whole;
         const double us = cdiv(whole, 256) * 1.6 * nk + (whole ? 12 : 0) + (rest ? 6 + tile_us(kMiddle, 4.0 * rest, nk) : 0);
-        if (whole && us < least) best = Plan{kLarge, 1};
+        if (whole && us < least) best = Plan{kLarge, 1, rest <= 64};      // (alone: the rest)
     } else {
-        best = Plan{kLarge, 1};
+        best = Plan{kLarge, 1, false};
     }
     return best;
 }
@@ -629,34 +657,51 @@ hipError_t join_shares(const Bf16Problem& p, int split, hipStream_t st) {
     return hipGetLastError();
 }
 
-hipError_t launch_jobs(GradJobs& j, bool small_d, hipStream_t st) {
+// d: the data gradient's plan (its tiles, or what the large kernel leaves).
+hipError_t launch_jobs(GradJobs& j, const Plan& d, hipStream_t st) {
     const int grid = j.nd + j.nw + j.ns + j.nr;
     if (grid == 0) return hipSuccess;
-    if (small_d) hipLaunchKernelGGL(bf16_grad_kernel<1>, dim3(grid), dim3(256), 0, st, j);
-    else hipLaunchKernelGGL(bf16_grad_kernel<2>, dim3(grid), dim3(256), 0, st, j);
+    const bool small = j.nd && d.kind == kSmall, alone = j.nd && !j.nw && d.alone;
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, st, j); };
+    if (alone) small ? go(bf16_grad_kernel<1, 3>) : go(bf16_grad_kernel<2, 3>);
+    else small ? go(bf16_grad_kernel<1, 2>) : go(bf16_grad_kernel<2, 2>);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_lora_product(const Bf16Problem& p, hipStream_t st) {
+hipError_t launch_lora_product(const Bf16Problem& p, const LoraDown& d, hipStream_t st) {
     const Plan q = plan_of(p);
     const dim3 bd(256);
+    // The adapters' part in the tiles shares each adapter's b among up to 32 rows, in the
+    // join of a split K every row reads its own.
+    const bool join_lr = q.split > 1 && p.M * p.N * p.lr.r <= (int64_t)1 << 25;
+    // then h can be made beside the tiles
+    const bool with_down = join_lr && !d.order && p.M * d.r <= kDownFine;
+    hipError_t e = with_down ? hipSuccess : launch_lora_down(d, st);
+    if (e != hipSuccess) return e;
     if (q.kind == kLarge) {
-        const hipError_t e = launch_bf16_large(p, true, st);
+        e = launch_bf16_large(p, true, st);
         if (e != hipSuccess) return e;
         const SmallArgs rest{p, 1, true, bf16_large_grid()};
-        hipLaunchKernelGGL(bf16_forward_kernel<2>, dim3(kRestGrid), bd, 0, st, rest);
+        if (q.alone) hipLaunchKernelGGL((bf16_forward_kernel<2, 3>), dim3(kRestGrid), bd, 0, st, rest);
+        else hipLaunchKernelGGL((bf16_forward_kernel<2, 2>), dim3(kRestGrid), bd, 0, st, rest);
         return hipGetLastError();
     }
-    // The adapters' part in the tiles shares each adapter's b among up to 32 rows, in the
-    // join every row reads its own.
-    const bool join_lr = q.split > 1 && p.M * p.N * p.lr.r <= (int64_t)1 << 25;
     const SmallArgs a{p, q.split, !join_lr, 0};
-    const dim3 gd((unsigned)small_grid(p, q));
-    if (q.kind == kSmall) hipLaunchKernelGGL(bf16_forward_kernel<1>, gd, bd, 0, st, a);
-    else hipLaunchKernelGGL(bf16_forward_kernel<2>, gd, bd, 0, st, a);
-    const hipError_t e = hipGetLastError();
+    const int tiles = (int)small_grid(p, q);
+    const bool small = q.kind == kSmall;
+    if (with_down) {
+        const dim3 gd((unsigned)(tiles + cdiv(p.M, 16) * d.r));
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, gd, bd, 0, st, a, d, tiles); };
+        if (q.alone) small ? go(bf16_forward_down_kernel<1, 3>) : go(bf16_forward_down_kernel<2, 3>);
+        else small ? go(bf16_forward_down_kernel<1, 2>) : go(bf16_forward_down_kernel<2, 2>);
+    } else {
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(tiles), bd, 0, st, a); };
+        if (q.alone) small ? go(bf16_forward_kernel<1, 3>) : go(bf16_forward_kernel<2, 3>);
+        else small ? go(bf16_forward_kernel<1, 2>) : go(bf16_forward_kernel<2, 2>);
+    }
+    e = hipGetLastError();
     if (e != hipSuccess || q.split == 1) return e;
     const dim3 gj((unsigned)cdiv(p.N, 1024), (unsigned)(p.M < 65535 ? p.M : 65535));
     auto join = [&](auto kernel) {
@@ -699,7 +744,7 @@ hipError_t launch_linear_grads(const Bf16Problem* d, const Bf16Problem* w, const
         j.s = sr;
         j.ns = (int)(sr.M < 512 ? sr.M : 512);
     }
-    e = launch_jobs(j, d_tiles && pd.kind == kSmall, st);
+    e = launch_jobs(j, pd, st);
     if (e == hipSuccess && d_tiles && pd.split > 1) e = join_shares(*d, pd.split, st);
     if (e != hipSuccess) return e;
     GradJobs k{};
@@ -715,7 +760,7 @@ hipError_t launch_linear_grads(const Bf16Problem* d, const Bf16Problem* w, const
         k.dr_parts = (int)bf16_dr_parts(d->N);
         k.nr = (int)cdiv(d->M, 256);
     }
-    e = launch_jobs(k, false, st);
+    e = launch_jobs(k, pd, st);
     if (e == hipSuccess && w && !w_tiles) e = launch_bf16_large(*w, false, st);
     if (e == hipSuccess && w_tiles && pw.split > 1) e = join_shares(*w, pw.split, st);
     return e;

@@ -271,19 +271,26 @@ int64_t bf16_dr_parts(int64_t N);
 // whole_rounds; the rest is then the middle tiles'), bf16_large_grid() workgroups.
 int bf16_large_grid();
 hipError_t launch_bf16_large(const Bf16Problem& p, bool tail, hipStream_t s);
-// kForward with its adapters.
-hipError_t launch_lora_product(const Bf16Problem& p, hipStream_t s);
+// h [M][2 r] = scale[id] x a[id]^T as high and low bf16 parts (rows without an
+// adapter are not written); a [L][r][K], K % 32 == 0, r % 8 == 0.  order: row m is row
+// order[m] of x, or null.
+struct LoraDown {
+    const uint16_t* x;
+    int64_t M, K;
+    const uint16_t* a;
+    const int32_t *ids, *order;
+    const float* scale;
+    int L, r;
+    uint16_t* h;
+};
+hipError_t launch_lora_down(const LoraDown& p, hipStream_t s);
+// kForward with its adapters, their h made by d.
+hipError_t launch_lora_product(const Bf16Problem& p, const LoraDown& d, hipStream_t s);
 // The data gradient d and the weight gradient w (either may be null).  scaled (or null):
 // an operand of w that is made first, bf16(scale_r[row] scale_x), [w->rows][scale_cols],
 // scale_cols % 8 == 0.  Both have parts of their own.
 hipError_t launch_linear_grads(const Bf16Problem* d, const Bf16Problem* w, const uint16_t* scale_x,
                                const float* scale_r, int64_t scale_cols, uint16_t* scaled, hipStream_t s);
-// h [M][2 r] = scale[id] x a[id]^T as high and low bf16 parts (rows without an
-// adapter are not written); a [L][r][K], K % 32 == 0, r % 8 == 0.  order: row m is row
-// order[m] of x, or null.
-hipError_t launch_lora_down(const uint16_t* x, int64_t M, int64_t K, const uint16_t* a,
-                            const int32_t* id, const int32_t* order, const float* scale, int L, int r,
-                            uint16_t* h, hipStream_t s);
 // y [M][N] = x w^T + the adapters' part for up to kLoraFewRows rows, N % 16 == 0.  Where
 // lora_fuses, h is made here of a and scale (lr.h is then not read).
 constexpr int kLoraFewRows = 16;
