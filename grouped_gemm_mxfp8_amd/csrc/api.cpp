@@ -752,7 +752,7 @@ mx_status check_lora_sizes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r
     if (K > kBf16MaxDim || N > kBf16MaxDim || M > kI32Max || r > MX_LORA_MAX_RANK)
         return fail(MX_ERR_UNSUPPORTED,
                     "lora_linear_fwd: needs K and N up to 2^21, M below 2^31 and r up to %d", MX_LORA_MAX_RANK);
-    if (mx::bf16_product_tiles(lora_problem(M, N, K)) > mx::kMaxBf16Tiles || (M + 15) / 16 > mx::kMaxBf16Tiles / 2)
+    if (mx::bf16_product_tiles(lora_problem(M, N, K)) > mx::kMaxBf16Tiles || (M + 15) / 16 > mx::kMaxBf16Tiles)
         return fail(MX_ERR_UNSUPPORTED, "lora_linear_fwd: too large for one launch");
     return MX_OK;
 }

@@ -262,8 +262,9 @@ struct Bf16Problem {
 };
 // Rows of the C matrix of each group are M of kWeightGrad, the group's rows else.
 // floats of `parts` the product takes (0: no split), workgroups of its launch (limit
-// kMaxBf16Tiles), rows of drp.
-constexpr int64_t kMaxBf16Tiles = (int64_t)1 << 23;
+// kMaxBf16Tiles: two products' of 256 threads each stay below the 2^32 of a launch), rows
+// of drp.
+constexpr int64_t kMaxBf16Tiles = (int64_t)1 << 22;
 int64_t bf16_product_tiles(const Bf16Problem& p);
 int64_t bf16_parts(const Bf16Problem& p);
 int64_t bf16_dr_parts(int64_t N);

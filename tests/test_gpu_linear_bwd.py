@@ -86,28 +86,34 @@ LARGE = [
     ([4097], 16, 4128), ([2500, 0, 3, 1700, 300], 80, 4096), ([4000, 130, 257], 208, 4384),
     ([900, 0, 5000, 129], 144, 4640), ([0, 70, 129, 700, 0, 1], 2064, 2848), ([1500, 10], 4112, 3616),
 ]
+# weight gradients of the large kernel: one expert's round, and many experts' chains of
+# sums of no, one, two and more steps
+LARGE_W = [([700], 3600, 3616), (([0, 1, 64, 65, 0, 0, 129, 200, 3, 300] * 4)[:32], 16, 8192),
+           (([70, 0, 1, 128, 0, 333, 40] * 5)[:31], 272, 4128)]
 
 
 @pytest.mark.parametrize("scaled", [False, True])
-@pytest.mark.parametrize("counts,N,K", SHAPES + LARGE)
+@pytest.mark.parametrize("counts,N,K", SHAPES + LARGE + LARGE_W)
 def test_against_fp64(dev, counts, N, K, scaled):
     dy, x, w, off, offd, r = make(counts, N, K, N + K, dev, scaled)
     nws = gm.lib().grouped_linear_bwd_ws_bytes(len(counts), x.shape[0], N, K, scaled)
     ws = torch.full((nws,), 255, dtype=torch.uint8, device=dev)
     dx, dw, dr = gm.grouped_linear_bwd(dy, x, offd, w, row_scale=r, ws=ws)
     dx2, dw2, dr2 = gm.grouped_linear_bwd(dy, x, offd, w, row_scale=r, dw_dtype=torch.float32)
+    dx3, none, dr3 = gm.grouped_linear_bwd(dy, x, offd, w, row_scale=r, need_dw=False)
     torch.cuda.synchronize()
     check(dy, x, w, off, r, dx, dw, dr)
     check(dy, x, w, off, r, None, dw2, None)
-    assert torch.equal(dx, dx2) and torch.equal(dw2.bfloat16(), dw)   # one order of the sums
-    assert (dr is None and dr2 is None) if r is None else torch.equal(dr, dr2)
+    # one order of the sums, whatever is asked for beside
+    assert torch.equal(dx, dx2) and torch.equal(dx, dx3) and torch.equal(dw2.bfloat16(), dw) and none is None
+    assert (dr is None and dr2 is None) if r is None else torch.equal(dr, dr2) and torch.equal(dr, dr3)
     for e, c in enumerate(counts):
         assert c or not dw[e].any()
 
 
 @pytest.mark.parametrize("scaled", [False, True])
 @pytest.mark.parametrize("counts,N,K", [([3, 0, 1], 48, 96), ([300, 0, 17, 511], 336, 256),
-                                        ([2000, 5], 16, 2048)])
+                                        ([2000, 5], 16, 2048)] + LARGE_W)
 def test_adding_to_a_gradient_buffer(dev, counts, N, K, scaled):
     dy, x, w, off, offd, r = make(counts, N, K, 3 * N + K, dev, scaled)
     buf = torch.randn(w.shape, generator=torch.Generator().manual_seed(1)).to(dev)
@@ -193,6 +199,30 @@ def test_what_is_not_finite_stays_in_its_row_and_expert(dev, counts, N, K):
     keep = torch.ones(N, dtype=torch.bool)
     keep[3] = False
     assert torch.equal(dw[0][keep][:, :7], clean[1][0][keep][:, :7])
+
+
+def test_offsets_past_32_bits(dev):
+    """x and dx of 4.4 GB, then weights and their gradient of 4.3 GB: the last rows and the
+    last expert."""
+    g = torch.Generator(device=dev).manual_seed(3)
+    M, N, K = 270000, 16, 8192
+    x = torch.randn((M, K), generator=g, device=dev, dtype=torch.bfloat16)
+    dy = torch.randn((M, N), generator=g, device=dev, dtype=torch.bfloat16)
+    w = torch.randn((2, N, K), generator=g, device=dev, dtype=torch.bfloat16)
+    off = np.array([0, M - 300, M])
+    dx, dw, dr = gm.grouped_linear_bwd(dy, x, torch.from_numpy(off).to(dev), w,
+                                       row_scale=torch.ones(M, device=dev))
+    tail = slice(M - 300, M)
+    check(dy[tail], x[tail], w[1:], np.array([0, 300]), torch.ones(300), dx[tail], dw[1:], dr[tail])
+    del x, dx, dy, dw, dr
+    E, N, K = 65, 4096, 8064
+    w = torch.empty((E, N, K), dtype=torch.bfloat16, device=dev).normal_(generator=g)
+    off = np.array([0] * (E - 1) + [3, 50])
+    x = torch.randn((50, K), generator=g, device=dev, dtype=torch.bfloat16)
+    dy = torch.randn((50, N), generator=g, device=dev, dtype=torch.bfloat16)
+    dx, dw, _ = gm.grouped_linear_bwd(dy, x, torch.from_numpy(off).to(dev), w)
+    check(dy[3:], x[3:], w[-1:], np.array([0, 47]), None, dx[3:], dw[-1:], None)
+    assert not dw[0].any() and not dw[E - 3].any()
 
 
 @pytest.mark.parametrize("counts,N,K", [([33, 0, 60], 80, 96), ([900, 300], 784, 544)])

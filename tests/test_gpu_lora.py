@@ -102,6 +102,30 @@ def test_row_counts(dev, M):
     assert (y[M:] == 7).all()                       # rows behind the last are left alone
 
 
+@pytest.mark.parametrize("M", [1, 12, 100, 700])
+def test_adapters_past_32_bits(dev, M):
+    """b of 4.8 GB, a of 0.2: rows of the last adapters."""
+    g = torch.Generator(device=dev).manual_seed(M)
+    K, N, r, L = 512, 16400, 480, 305
+    rnd = lambda *s: torch.randn(s, generator=g, device=dev, dtype=torch.bfloat16)
+    x, w, a = rnd(M, K), rnd(N, K), rnd(L, r, K)
+    b = torch.empty((L, N, r), dtype=torch.bfloat16, device=dev).normal_(generator=g)
+    ids = (torch.arange(M, device=dev) % 3 + L - 3).int()
+    y = gm.lora_linear_fwd(x, w, a, b, ids)
+    torch.cuda.synchronize()
+    rows = torch.arange(0, M, max(1, M // 12), device=dev)
+    check(y[rows], x[rows], w, a[-3:], b[-3:], ids[rows] - (L - 3), None)
+
+
+def test_a_row_is_the_same_wherever_it_stands(dev):
+    """Rows of a sorted batch in another order: the same bits for each row."""
+    x, w, a, b, ids, s = make(900, 544, 784, 16, 6, "mixed", 5, dev)
+    y = gm.lora_linear_fwd(x, w, a, b, ids, scale=s)
+    for seed in range(3):
+        p = torch.randperm(900, generator=torch.Generator().manual_seed(seed)).to(dev)
+        assert torch.equal(gm.lora_linear_fwd(x[p], w, a, b, ids[p], scale=s), y[p])
+
+
 @pytest.mark.parametrize("M", [4, 90, 900])
 def test_captured_and_replayed(dev, M):
     x, w, a, b, ids, s = make(M, 544, 784, 16, 6, "mixed", M, dev)
@@ -124,7 +148,7 @@ def test_captured_and_replayed(dev, M):
 
 
 def test_two_streams_at_once(dev):
-    cases = [make(M, 1024, 784, 16, 6, "mixed", M, dev) for M in (7, 300)]
+    cases = [make(M, 1024, 784, 16, 6, "mixed", M, dev) for M in (7, 300, 1500)]
     refs = [gm.lora_linear_fwd(x, w, a, b, ids, scale=s) for x, w, a, b, ids, s in cases]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in cases]
