@@ -8,11 +8,15 @@
 // so one barrier a step is enough: behind it the next step's stage has landed and this
 // step's, already read, is refilled.  (With the reads in the half of a step that follows
 // a second barrier, as registers allow the large kernel, that half is bound by the LDS:
-// 6 to 10 % slower here.)  Two stages let two workgroups share a CU and hide each other's
-// waits; a launch of at most one workgroup a CU takes three (256 tiles of 64 x 128, K =
-// 4096: 31 us, with two stages 40).  Where the tiles alone leave CUs idle, K is cut into
-// `split` shares, whose fp32 sums go to memory and are added in order by a second launch:
-// one order of every sum, no atomics.
+// 6 to 10 % slower here.)  Two workgroups share a CU and hide each other's waits, with three
+// stages (small tiles) or two (middle ones); a launch of at most one middle tile a CU takes
+// four (1024 rows of 4096 x 4096: 38 us, with two stages 47).  Loading a middle tile's step
+// takes a CU 0.25 us, its MFMAs 0.21 and the LDS about as long, and one wave a SIMD has to
+// issue all of it: 0.48 us.  So the code of a step holds nothing that could be left out:
+// stages are constants (75 instructions for 16 MFMAs; with stages counted, 127 and 0.56
+// us), and the end of K is dealt with once, in the last step.  Where the tiles alone leave
+// CUs idle, K is cut into `split` shares, whose fp32 sums go to memory and are added in
+// order by a second launch: one order of every sum, no atomics.
 //
 // LDS orders (64 banks of 4 bytes): along K, chunk c of line n is stored at
 // c ^ (n >> 1 & 7); across K, the 64-byte quarter of a 256-byte row at quarter ^ (k & 3),
@@ -41,6 +45,7 @@ __device__ __forceinline__ v4i across_rsrc(const uint16_t* p, int64_t k0, int64_
 }
 
 constexpr int small_stage(int MB) { return small_m(MB) * 128 + SM_B; }
+constexpr int per_cu(int MB, int ST) { return 2 * ST * small_stage(MB) <= 160 * 1024 ? 2 : 1; }
 
 // What workgroup `block` (of a multiple of 128) of a product's does.
 template <Bf16Form F, int MB, int ST>
@@ -49,7 +54,7 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
     constexpr int SM_M = small_m(MB), SM_A = SM_M * 128, SM_STAGE = small_stage(MB);
     constexpr int SM_LOADS = 2 * MB + 4;                  // per wave and step, of A and B
     constexpr int SLOTS = 8 * MB, READS = 4 * (MB + 2);   // of a step: MFMAs, fragments
-    constexpr int WAIT = 2 * MB;                          // MFMAs before its barrier
+    constexpr int WAIT = MB;                          // MFMAs before its barrier
     constexpr bool kA = F != Bf16Form::kWeightGrad;       // A lies along K
     constexpr bool kB = F == Bf16Form::kForward;          // B lies along K
     constexpr bool kRows = F != Bf16Form::kWeightGrad;    // groups own rows of C
@@ -62,8 +67,7 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
     // ---- the workgroup's tile and share of K ----
     int g = 0;
     int64_t m0, mvalid, n0, row0 = 0, krows = p.K;
-    // tiles there are (the grid is a multiple of 8 and may be larger: the rows of groups
-    // are on the device)
+    // tiles there are (the grid may be larger: the rows of groups are on the device)
     const bool rest = kRows && MB == 2 && s.rounds;       // quarters of what the large kernel left
     const int ntl = (int)((p.N + 255) / 256);
     int mtiles = 0, units, left = 0;
@@ -157,27 +161,25 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
     const uint32_t brow = (uint32_t)((kB ? 8 : 4) * ldb * 2);
     struct Rsrc {
         v4i a, b;
-        uint32_t soff, o0, o1;
+        uint32_t soff;
     };
-    // descriptors of step ks; along K the lanes whose chunk lies past K load nothing
+    // descriptors of step ks.  (Along K the lanes of a last step whose chunk lies past K
+    // load what follows; its MFMAs leave that out.)
     auto rsrc_of = [&](int ks) -> Rsrc {
-        const bool live = ks < k_end;
-        auto rng = [&](const v4i& r) { return live ? r : v4i{r.x, r.y, 0, r.w}; };
-        const int64_t left = p.K - (int64_t)ks * SM_K;
-        return Rsrc{rng(kA ? ra : across_rsrc(Ag, (int64_t)ks * SM_K, krows, lda, m0)),
-                    rng(kB ? rb : across_rsrc(Bg, (int64_t)ks * SM_K, krows, ldb, n0)), (uint32_t)ks * 128u,
-                    ac * 8 < left ? 0u : 0x80000000u, (ac ^ 4) * 8 < left ? 0u : 0x80000000u};
+        Rsrc r{kA ? ra : across_rsrc(Ag, (int64_t)ks * SM_K, krows, lda, m0),
+               kB ? rb : across_rsrc(Bg, (int64_t)ks * SM_K, krows, ldb, n0), (uint32_t)ks * 128u};
+        r.a.z = ks < k_end ? r.a.z : 0;
+        r.b.z = ks < k_end ? r.b.z : 0;
+        return r;
     };
     auto dma = [&](auto uc, const Rsrc& r, int st) {
         constexpr int u = decltype(uc)::value;
         const uint32_t at = smb + (uint32_t)st * SM_STAGE;
         if constexpr (u < 2 * MB) {
-            dma_b128<u * 1024>(r.a, at + wave * (2048 * MB), kA ? aoff[u] | (u & 1 ? r.o1 : r.o0) : aoff[u],
-                               kA ? r.soff : 0u);
+            dma_b128<u * 1024>(r.a, at + wave * (2048 * MB), aoff[u], kA ? r.soff : 0u);
         } else {
             constexpr int v = u - 2 * MB;
-            const uint32_t off = boff + v * brow + (v & 1 ? bflip : 0u);
-            dma_b128<v * 1024>(r.b, at + SM_A + wave * 4096, kB ? off | (v & 1 ? r.o1 : r.o0) : off, kB ? r.soff : 0u);
+            dma_b128<v * 1024>(r.b, at + SM_A + wave * 4096, boff + v * brow + (v & 1 ? bflip : 0u), kB ? r.soff : 0u);
         }
     };
 
@@ -217,9 +219,8 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
         if constexpr (w < 2) f.b[w][kk] = frag_b(st, w, kk);
         else f.a[w - 2][kk] = frag_a(st, w - 2, kk);
     };
-    auto step = [&](int ks, Frags& cur, Frags& nxt) {
-        const int st = (ks - k_beg) % ST;
-        const uint8_t* const from = sm[(ks + 1 - k_beg) % ST];
+    auto step = [&](auto stc, int ks, Frags& cur, Frags& nxt) {
+        constexpr int st = decltype(stc)::value;
         const Rsrc r = rsrc_of(ks + ST);
         static_for<SLOTS>([&](auto tc) {
             constexpr int t = decltype(tc)::value, kk = t / (2 * MB), i = t / 2 % MB, j = t % 2;
@@ -231,43 +232,70 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
             acc[i][j] = mfma_bf16(cur.b[j][kk], cur.a[i][kk], acc[i][j]);
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (at >= 0) {
-                constexpr int per = (READS + SLOTS - WAIT - 2) / (SLOTS - WAIT - 1);   // none in the last
-                static_for<per>([&](auto uc) {
-                    constexpr int n = at * per + decltype(uc)::value;
-                    if constexpr (n < READS) read(std::integral_constant<int, n>{}, nxt, from);
+                // spread evenly (no read in the last slot)
+                constexpr int RS = SLOTS - WAIT - 1, LS = SLOTS - WAIT;
+                static_for<(READS + RS - 1) / RS>([&](auto uc) {
+                    constexpr int n = (at * READS + RS - 1) / RS + decltype(uc)::value;
+                    if constexpr (n < READS && n * RS < (at + 1) * READS)
+                        read(std::integral_constant<int, n>{}, nxt, sm[(st + 1) % ST]);
                 });
-                constexpr int lper = (SM_LOADS + SLOTS - WAIT - 1) / (SLOTS - WAIT);
-                static_for<lper>([&](auto uc) {
-                    constexpr int n = at * lper + decltype(uc)::value;
-                    if constexpr (n < SM_LOADS) dma(std::integral_constant<int, n>{}, r, st);
+                static_for<(SM_LOADS + LS - 1) / LS>([&](auto uc) {
+                    constexpr int n = (at * SM_LOADS + LS - 1) / LS + decltype(uc)::value;
+                    if constexpr (n < SM_LOADS && n * LS < (at + 1) * SM_LOADS)
+                        dma(std::integral_constant<int, n>{}, r, st);
                 });
             }
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    Frags f0, f1;
-    {
-        const Rsrc r0 = rsrc_of(k_beg);
-        static_for<SM_LOADS>([&](auto uc) { dma(uc, r0, 0); });
-        if (k_beg + 1 < k_end) {
-            static_for<ST - 1>([&](auto ic) {
-                constexpr int i = decltype(ic)::value + 1;
-                const Rsrc r1 = rsrc_of(k_beg + i);
-                static_for<SM_LOADS>([&](auto uc) { dma(uc, r1, i); });
+    // The last one: sixteens of K up to the end of an operand along K (others are zeros).
+    auto last = [&](const Frags& cur) {
+        const int64_t left = p.K - (int64_t)(k_end - 1) * SM_K;
+        static_for<4>([&](auto kc) {
+            constexpr int kk = decltype(kc)::value;
+            if (kk > 0 && kA && 16 * kk >= left) return;
+            static_for<MB>([&](auto ic) {
+                constexpr int i = decltype(ic)::value;
+                acc[i][0] = mfma_bf16(cur.b[0][kk], cur.a[i][kk], acc[i][0]);
+                acc[i][1] = mfma_bf16(cur.b[1][kk], cur.a[i][kk], acc[i][1]);
             });
-            wait_vm<(ST - 1) * SM_LOADS>();
-        } else {
-            wait_vm<0>();
-        }
-        lds_barrier();
+        });
+    };
+    // Steps go in pairs, with stages that the code holds as constants, up to one that is
+    // left: with an even number of them the first goes alone, in the last stage.
+    Frags f0, f1;
+    const bool even = ((k_end - k_beg) & 1) == 0;
+    auto fill = [&](int i) {                      // step k_beg + i
+        const Rsrc r = rsrc_of(k_beg + i);
+        const int st = even ? (i + ST - 1) % ST : i;
+        static_for<SM_LOADS>([&](auto uc) { dma(uc, r, st); });
+    };
+    fill(0);
+    if (k_beg + 1 < k_end) {
+#pragma unroll
+        for (int i = 1; i < ST; ++i) fill(i);
+        wait_vm<(ST - 1) * SM_LOADS>();
+    } else {
+        wait_vm<0>();
+    }
+    lds_barrier();
+    int ks = k_beg;
+    if (even) {
+        static_for<READS>([&](auto nc) { read(nc, f1, sm[ST - 1]); });
+        if (ks < k_end) step(std::integral_constant<int, ST - 1>{}, ks++, f1, f0);
+    } else {
         static_for<READS>([&](auto nc) { read(nc, f0, sm[0]); });
     }
-    int ks = k_beg;
-    for (; ks + 2 <= k_end; ks += 2) {
-        step(ks, f0, f1);
-        step(ks + 1, f1, f0);
+    while (ks + 1 < k_end) {
+        static_for<ST % 2 ? ST : ST / 2>([&](auto uc) {
+            constexpr int u = 2 * decltype(uc)::value;
+            if (u && ks + 1 >= k_end) return;
+            step(std::integral_constant<int, u % ST>{}, ks, f0, f1);
+            step(std::integral_constant<int, (u + 1) % ST>{}, ks + 1, f1, f0);
+            ks += 2;
+        });
     }
-    if (ks < k_end) step(ks, f0, f1);
+    if (ks < k_end) last(f0);
     wait_vm<0>();          // no load may still be landing in LDS when the workgroup ends
 
     // ---- output: the wave's blocks of 32 x 64 ----
@@ -330,7 +358,7 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
 }
 
 template <int MB, int ST>
-__global__ void __launch_bounds__(256, ST == 2 ? 2 : 1)
+__global__ void __launch_bounds__(256, per_cu(MB, ST))
 bf16_forward_kernel(SmallArgs s) {
     __shared__ __attribute__((aligned(16))) uint8_t sm[ST][small_stage(MB)];
     small_tile<Bf16Form::kForward, MB, ST>(s, (int)blockIdx.x, sm);
@@ -339,7 +367,7 @@ bf16_forward_kernel(SmallArgs s) {
 // The same with the adapters' down projection in the workgroups from `tiles` on, for calls
 // whose join adds the adapters' part.
 template <int MB, int ST>
-__global__ void __launch_bounds__(256, ST == 2 ? 2 : 1)
+__global__ void __launch_bounds__(256, per_cu(MB, ST))
 bf16_forward_down_kernel(SmallArgs s, LoraDown d, int tiles) {
     union Smem {
         uint8_t tile[ST][small_stage(MB)];
@@ -512,16 +540,17 @@ struct GradJobs {
 };
 // MB and ST are the data gradient's.
 template <int MB, int ST>
-__global__ void __launch_bounds__(256, ST == 2 ? 2 : 1)
+__global__ void __launch_bounds__(256, per_cu(MB, ST))
 bf16_grad_kernel(GradJobs j) {
+    constexpr bool with_w = per_cu(MB, ST) == 2;    // (weight gradients always share CUs)
     union Smem {
-        uint8_t d[ST][small_stage(MB)], w[ST == 2 ? 2 : 1][small_stage(2)];
+        uint8_t d[ST][small_stage(MB)], w[with_w ? 2 : 1][small_stage(2)];
     };
     __shared__ __attribute__((aligned(16))) Smem sm;
     int b = (int)blockIdx.x;
     if (b < j.nd) return small_tile<Bf16Form::kDataGrad, MB, ST>(j.d, b, sm.d);
     b -= j.nd;
-    if constexpr (ST == 2) {                       // (a launch with both has no need of three)
+    if constexpr (with_w) {
         if (b < j.nw) return small_tile<Bf16Form::kWeightGrad, 2, 2>(j.w, b, sm.w);
         b -= j.nw;
     }
@@ -552,50 +581,56 @@ enum Kind { kLarge = 0, kSmall = 1, kMiddle = 2 };     // (kSmall, kMiddle: also
 struct Plan {
     Kind kind;
     int split;
-    bool alone = false;    // at most one workgroup a CU
+    bool alone = false;    // middle tiles, at most one workgroup a CU: four stages
 };
 
 // Rows of groups are on the device: groups are taken as equal here.
 //
 // Products whose groups own rows: the fastest by a model of their times, in us, its
-// numbers measured at K x N of 4096 x 4096, 1408 x 2064, 4096 x 14336 and 1024 x 1024
-// with 17 to 8192 rows, and at 1 to 64 experts with 4 to 4096 rows each.  A tile's step
-// of 64 in K takes a CU 0.4 (small) or 0.56 (middle) for a workgroup alone, 0.34 or 0.52 a
-// workgroup when it has several, and 1.6 (large, four middle ones' work); starting and
-// storing take 6, a large round 12 in all; adding the shares of a split K takes 4.5 and
+// numbers measured at K x N of 4096 x 4096, 1408 x 2064, 4096 x 14336, 14336 x 4096 and
+// 1024 x 1024 with 17 to 8192 rows, and at 1 to 64 experts with 4 to 4096 rows each.  A
+// tile's step of 64 in K takes a CU 0.31 (small) or 0.48 (middle) for a workgroup alone, 0.30
+// or 0.47 a workgroup when it has several, and 1.6 (large, four middle ones' work); starting
+// and storing take 6, a large round 12 in all; adding the shares of a split K takes 4.5 and
 // the time its bytes need.  A last round of large tiles goes to middle ones where
-// whole_rounds says so.
+// whole_rounds says so.  The adapters' down projection of few rows takes half of the CUs
+// beside the tiles of a split K (K x N = 14336 x 4096, 128 rows, middle tiles: 256 of them 59
+// us, 128 37), or a launch of its own of K / 512.
 Plan plan_rows(const Bf16Problem& p) {
     const int64_t groups = p.form == Bf16Form::kForward ? 1 : p.rows < p.G ? p.rows : p.G;
     const int64_t rows = groups ? cdiv(p.rows, groups) : 0;
     const double nk = (double)cdiv(p.K, SM_K);
     auto tiles = [&](int bm, int bn) { return (double)(groups * cdiv(rows, bm) * cdiv(p.N, bn)); };
-    auto tile_us = [&](Kind k, double units, double steps) {
-        const double each = units / 256;
-        return each <= 1 ? steps * (k == kSmall ? 0.4 : 0.56) : steps * (k == kSmall ? 0.34 : 0.52) * (each < 2 ? 2 : each);
+    const bool beside = p.form == Bf16Form::kForward && p.rows <= kLoraUnsorted;
+    auto tile_us = [&](Kind k, double units, double steps, double cus) {
+        const double each = units / cus, most = units <= 2 * cus ? 2 : (double)(((int64_t)units - 1) / (int64_t)cus + 1);
+        if (k == kSmall) return steps * (each <= 1 ? 0.31 : 0.30 * most);
+        return steps * (each <= 1 ? 0.48 : each <= 2 ? 0.37 + 0.27 * each : 0.47 * most);
     };
     Plan best{kSmall, 1};
     double least = 1e30;
     for (Kind k : {kSmall, kMiddle}) {
         const double t = tiles(small_m(k), SM_N);
         for (int split = 1; split <= 16 && nk >= 4.0 * split && t * split <= 1024; ++split) {
-            double us = 6 + tile_us(k, t * split, nk / split);
+            double us = 6 + tile_us(k, t * split, nk / split, beside && split > 1 ? 128 : 256);
+            if (beside && split == 1) us += p.K / 512;
             if (split > 1) us += 4.5 + 8e-6 * split * p.rows * p.N / 3;
             if (us < least) {
                 least = us;
                 best = Plan{k, split, small_tiles(p, k) * split <= 256};
             }
         }
-        if (t > 1024 && 6 + tile_us(k, t, nk) < least) {
-            least = 6 + tile_us(k, t, nk);
+        const double whole = 6 + tile_us(k, t, nk, 256);
+        if (t > 1024 && whole < least) {
+            least = whole;
             best = Plan{k, 1, false};
         }
     }
     const double t = tiles(256, 256);
     if (t < 1e9) {
         const int whole = whole_rounds((int)t, 256), rest = (int)t - whole;
-        const double us = cdiv(whole, 256) * 1.6 * nk + (whole ? 12 : 0) + (rest ? 6 + tile_us(kMiddle, 4.0 * rest, nk) : 0);
-        if (whole && us < least) best = Plan{kLarge, 1, rest <= 64};      // (alone: the rest)
+        const double us = cdiv(whole, 256) * 1.6 * nk + (whole ? 12 : 0) + (rest ? 6 + tile_us(kMiddle, 4.0 * rest, nk, 256) : 0);
+        if (whole && us < least) best = Plan{kLarge, 1, rest > 0 && rest <= 64};      // (alone: the rest)
     } else {
         best = Plan{kLarge, 1, false};
     }
@@ -643,7 +678,8 @@ int64_t bf16_dr_parts(int64_t N) { return cdiv(N, 64); }
 
 namespace {
 
-// Workgroups of the middle tiles that take what the large kernel left.
+// Workgroups of the middle tiles that take what the large kernel left, where only the
+// device knows how much.
 constexpr int kRestGrid = (4 * kTailMost + 127) / 128 * 128;
 
 hipError_t join_shares(const Bf16Problem& p, int split, hipStream_t st) {
@@ -661,10 +697,10 @@ hipError_t join_shares(const Bf16Problem& p, int split, hipStream_t st) {
 hipError_t launch_jobs(GradJobs& j, const Plan& d, hipStream_t st) {
     const int grid = j.nd + j.nw + j.ns + j.nr;
     if (grid == 0) return hipSuccess;
-    const bool small = j.nd && d.kind == kSmall, alone = j.nd && !j.nw && d.alone;
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, st, j); };
-    if (alone) small ? go(bf16_grad_kernel<1, 3>) : go(bf16_grad_kernel<2, 3>);
-    else small ? go(bf16_grad_kernel<1, 2>) : go(bf16_grad_kernel<2, 2>);
+    if (j.nd && d.kind == kSmall) go(bf16_grad_kernel<1, 3>);
+    else if (j.nd && !j.nw && d.alone) go(bf16_grad_kernel<2, 4>);
+    else go(bf16_grad_kernel<2, 2>);
     return hipGetLastError();
 }
 
@@ -683,23 +719,25 @@ hipError_t launch_lora_product(const Bf16Problem& p, const LoraDown& d, hipStrea
     if (q.kind == kLarge) {
         e = launch_bf16_large(p, true, st);
         if (e != hipSuccess) return e;
-        const SmallArgs rest{p, 1, true, bf16_large_grid()};
-        if (q.alone) hipLaunchKernelGGL((bf16_forward_kernel<2, 3>), dim3(kRestGrid), bd, 0, st, rest);
-        else hipLaunchKernelGGL((bf16_forward_kernel<2, 2>), dim3(kRestGrid), bd, 0, st, rest);
+        const int grid = bf16_large_grid(), all = (int)(cdiv(p.M, 256) * cdiv(p.N, 256));
+        const int left = (int)cdiv((all - whole_rounds(all, grid)) * 4, 128) * 128;
+        if (left == 0) return hipSuccess;
+        const SmallArgs rest{p, 1, true, grid};
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(left), bd, 0, st, rest); };
+        q.alone ? go(bf16_forward_kernel<2, 4>) : go(bf16_forward_kernel<2, 2>);
         return hipGetLastError();
     }
     const SmallArgs a{p, q.split, !join_lr, 0};
     const int tiles = (int)small_grid(p, q);
-    const bool small = q.kind == kSmall;
     if (with_down) {
         const dim3 gd((unsigned)(tiles + cdiv(p.M, 16) * d.r));
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, gd, bd, 0, st, a, d, tiles); };
-        if (q.alone) small ? go(bf16_forward_down_kernel<1, 3>) : go(bf16_forward_down_kernel<2, 3>);
-        else small ? go(bf16_forward_down_kernel<1, 2>) : go(bf16_forward_down_kernel<2, 2>);
+        if (q.kind == kSmall) go(bf16_forward_down_kernel<1, 3>);
+        else q.alone ? go(bf16_forward_down_kernel<2, 4>) : go(bf16_forward_down_kernel<2, 2>);
     } else {
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(tiles), bd, 0, st, a); };
-        if (q.alone) small ? go(bf16_forward_kernel<1, 3>) : go(bf16_forward_kernel<2, 3>);
-        else small ? go(bf16_forward_kernel<1, 2>) : go(bf16_forward_kernel<2, 2>);
+        if (q.kind == kSmall) go(bf16_forward_kernel<1, 3>);
+        else q.alone ? go(bf16_forward_kernel<2, 4>) : go(bf16_forward_kernel<2, 2>);
     }
     e = hipGetLastError();
     if (e != hipSuccess || q.split == 1) return e;

@@ -241,6 +241,7 @@ struct LowRank {
 };
 // Whether a call's rows are put in the order of their adapters: order and id come from
 // launch_lora_sort.
+constexpr int kLoraUnsorted = 256;     // up to so many rows never are
 bool lora_sorts(int64_t M, int64_t K, int L);
 hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int L, int32_t* order, int32_t* sorted_ids,
                             hipStream_t s);

@@ -244,7 +244,7 @@ hipError_t launch_lora_few(const uint16_t* x, int64_t M, int64_t K, const uint16
 
 // Where adapters have eight rows each on average; rows in 32-bit bytes.
 bool lora_sorts(int64_t M, int64_t K, int L) {
-    return M > 256 && M <= 65536 && L <= kSortMaxL && 8 * (int64_t)L <= M && M * K < ((int64_t)1 << 30);
+    return M > kLoraUnsorted && M <= 65536 && L <= kSortMaxL && 8 * (int64_t)L <= M && M * K < ((int64_t)1 << 30);
 }
 hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int L, int32_t* order, int32_t* sorted_ids,
                             hipStream_t s) {
