@@ -147,6 +147,48 @@ def test_captured_and_replayed(dev, M):
         assert torch.equal(got, ref)
 
 
+# few rows of a wide layer: x in the LDS, columns by a CU in one stream (and the sizes next to
+# those that take it)
+WIDE = [
+    (1, 2048, 12288, 16, 3, 2), (1, 2080, 12304, 32, 2, 0), (1, 2048, 12272, 16, 3, 1), (1, 2016, 12288, 16, 3, 1),
+    (2, 2080, 16400, 16, 4, "each"), (2, 2112, 12304, 24, 4, "each"), (4, 2144, 12352, 8, 5, "each"),
+    (5, 4096, 12304, 64, 9, "each"), (16, 4224, 12288, 8, 20, "each"), (16, 4256, 12288, 8, 20, "each"),
+    (16, 2336, 14336, 64, 30, "each"), (3, 20000, 12288, 8, 2, "each"), (1, 2048, 28672, 512, 2, 1),
+    (7, 2048, 12288, 16, 2, -1),
+]
+
+
+@pytest.mark.parametrize("M,K,N,r,L,ids", WIDE)
+def test_wide_layers(dev, M, K, N, r, L, ids):
+    x, w, a, b, ids, s = make(M, K, N, r, L, ids, M + K + N, dev)
+    nws = gm.lib().lora_linear_ws_bytes(M, N, K, L, r)
+    ws = torch.full((nws,), 255, dtype=torch.uint8, device=dev)
+    y = torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device=dev)
+    st = gm.lib().lora_linear_fwd(x.data_ptr(), M, K, w.data_ptr(), N, a.data_ptr(), b.data_ptr(), L, r,
+                                  ids.data_ptr(), s.data_ptr(), y.data_ptr(), ws.data_ptr(), ws.numel(),
+                                  torch.cuda.current_stream().cuda_stream)
+    assert st == 0, gm.last_error()
+    torch.cuda.synchronize()
+    check(y[:M], x, w, a, b, ids, s)
+    assert (y[M] == 7).all()
+    for _ in range(3):
+        assert torch.equal(y[:M], gm.lora_linear_fwd(x, w, a, b, ids, scale=s))
+
+
+@pytest.mark.parametrize("M,r", [(2, 16), (9, 40)])
+def test_wide_layers_keep_what_is_not_finite(dev, M, r):
+    x, w, a, b, ids, s = make(M, 2080, 12304, r, 3, "each", M, dev)
+    ids[0], ids[1] = 1, -1
+    clean = gm.lora_linear_fwd(x, w, a, b, ids, scale=s)
+    b[2] = float("nan")
+    a[2] = float("inf")
+    assert torch.equal(gm.lora_linear_fwd(x, w, a, b, ids, scale=s)[:2], clean[:2])
+    x[1, 2079] = float("nan")
+    y = gm.lora_linear_fwd(x, w, a, b, ids, scale=s)
+    torch.cuda.synchronize()
+    assert torch.equal(y[0], clean[0]) and y[1].isnan().all()
+
+
 def test_two_streams_at_once(dev):
     cases = [make(M, 1024, 784, 16, 6, "mixed", M, dev) for M in (7, 300, 1500)]
     refs = [gm.lora_linear_fwd(x, w, a, b, ids, scale=s) for x, w, a, b, ids, s in cases]
