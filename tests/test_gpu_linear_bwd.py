@@ -112,6 +112,17 @@ def test_against_fp64(dev, counts, N, K, scaled):
 
 
 @pytest.mark.parametrize("scaled", [False, True])
+def test_shares_of_a_long_sum(dev, scaled):
+    """dx over a long N, cut into shares of middle tiles."""
+    dy, x, w, off, offd, r = make([690, 10], 14336, 2048, 7, dev, scaled)
+    dx, dw, dr = gm.grouped_linear_bwd(dy, x, offd, w, row_scale=r)
+    dx1, _, dr1 = gm.grouped_linear_bwd(dy, x, offd, w, row_scale=r, need_dw=False)
+    torch.cuda.synchronize()
+    check(dy, x, w, off, r, dx, dw, dr)
+    assert torch.equal(dx, dx1) and (r is None or torch.equal(dr, dr1))
+
+
+@pytest.mark.parametrize("scaled", [False, True])
 @pytest.mark.parametrize("counts,N,K", [([3, 0, 1], 48, 96), ([300, 0, 17, 511], 336, 256),
                                         ([2000, 5], 16, 2048)] + LARGE_W)
 def test_adding_to_a_gradient_buffer(dev, counts, N, K, scaled):

@@ -154,7 +154,7 @@ WIDE = [
     (2, 2080, 16400, 16, 4, "each"), (2, 2112, 12304, 24, 4, "each"), (4, 2144, 12352, 8, 5, "each"),
     (5, 4096, 12304, 64, 9, "each"), (16, 4224, 12288, 8, 20, "each"), (16, 4256, 12288, 8, 20, "each"),
     (16, 2336, 14336, 64, 30, "each"), (3, 20000, 12288, 8, 2, "each"), (1, 2048, 28672, 512, 2, 1),
-    (7, 2048, 12288, 16, 2, -1),
+    (7, 2048, 12288, 16, 2, -1), (3, 4128, 12304, 24, 4, "each"), (16, 4128, 14336, 8, 20, "each"),
 ]
 
 
@@ -175,18 +175,29 @@ def test_wide_layers(dev, M, K, N, r, L, ids):
         assert torch.equal(y[:M], gm.lora_linear_fwd(x, w, a, b, ids, scale=s))
 
 
-@pytest.mark.parametrize("M,r", [(2, 16), (9, 40)])
-def test_wide_layers_keep_what_is_not_finite(dev, M, r):
-    x, w, a, b, ids, s = make(M, 2080, 12304, r, 3, "each", M, dev)
+@pytest.mark.parametrize("M,K,r", [(2, 2080, 16), (9, 4128, 40)])
+def test_wide_layers_keep_what_is_not_finite(dev, M, K, r):
+    x, w, a, b, ids, s = make(M, K, 12304, r, 3, "each", M, dev)
     ids[0], ids[1] = 1, -1
     clean = gm.lora_linear_fwd(x, w, a, b, ids, scale=s)
     b[2] = float("nan")
     a[2] = float("inf")
     assert torch.equal(gm.lora_linear_fwd(x, w, a, b, ids, scale=s)[:2], clean[:2])
-    x[1, 2079] = float("nan")
+    x[1, K - 1] = float("nan")
     y = gm.lora_linear_fwd(x, w, a, b, ids, scale=s)
     torch.cuda.synchronize()
     assert torch.equal(y[0], clean[0]) and y[1].isnan().all()
+
+
+# a long K in shares of middle tiles, more than a CU each: rows sorted, and as they are with
+# the down projection beside the tiles
+@pytest.mark.parametrize("L", [3, 90])
+def test_shares_of_a_long_sum(dev, L):
+    x, w, a, b, ids, s = make(700, 14336, 4096, 8, L, "each", L, dev)
+    y = gm.lora_linear_fwd(x, w, a, b, ids, scale=s)
+    torch.cuda.synchronize()
+    check(y, x, w, a, b, ids, s)
+    assert torch.equal(y, gm.lora_linear_fwd(x, w, a, b, ids, scale=s))
 
 
 def test_two_streams_at_once(dev):
