@@ -730,7 +730,7 @@ mx::Bf16Problem lora_problem(int64_t M, int64_t N, int64_t K) {
     return p;
 }
 struct LoraWs {
-    size_t h, order, ids, parts, total;
+    size_t h, order, ids, offs, parts, total;
 };
 LoraWs lora_ws(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r) {
     Carver c;
@@ -739,6 +739,7 @@ LoraWs lora_ws(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r) {
     W.h = c.take(M > mx::kLoraFewRows || !mx::lora_fuses(M, r) ? (size_t)(M * r) * 4 : 0);
     W.order = c.take(sorted);
     W.ids = c.take(sorted);
+    W.offs = c.take(sorted ? (size_t)(L + 1) * 8 : 0);
     W.parts = c.take(M > mx::kLoraFewRows ? (size_t)mx::bf16_parts(lora_problem(M, N, K)) * 4 : 0);
     W.total = needed_or_none(c.off);
     return W;
@@ -787,16 +788,18 @@ mx_status lora_linear_fwd(const void* x, int64_t M, int64_t K, const void* w, in
     mx::LowRank lr{h, static_cast<const uint16_t*>(b), d_ids, r, L, nullptr};
     const double flops = 2.0 * M * N * (K + r);    // (and 2 M r K of h)
     mx_status ls;
+    int64_t* offs = nullptr;
     if (mx::lora_sorts(M, K, L)) {
         int32_t *const to = reinterpret_cast<int32_t*>(base + W.order), *const sid = reinterpret_cast<int32_t*>(base + W.ids);
+        offs = reinterpret_cast<int64_t*>(base + W.offs);
         ls = launched(timed("lora_sort", 16.0 * M, MX_WORK_BYTES, s,
-                            [&] { return mx::launch_lora_sort(d_ids, M, L, to, sid, s); }),
+                            [&] { return mx::launch_lora_sort(d_ids, M, L, to, sid, offs, s); }),
                       "lora_sort");
         if (ls != MX_OK) return ls;
         lr.id = sid;
         lr.order = to;
     }
-    const mx::LoraDown down{x16, M, K, a16, lr.id, lr.order, d_scale, L, r, h};
+    const mx::LoraDown down{x16, M, K, a16, lr.id, lr.order, offs, d_scale, L, r, h};
     if (M <= mx::kLoraFewRows) {
         if (!mx::lora_fuses(M, r)) {
             ls = launched(timed("lora_down", 2.0 * M * r * K, MX_WORK_FLOP, s,

@@ -56,8 +56,9 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
     constexpr int SLOTS = 8 * MB, READS = 4 * (MB + 2);   // of a step: MFMAs, fragments
     constexpr int WAIT = MB;                          // MFMAs before its barrier
     constexpr bool kA = F != Bf16Form::kWeightGrad;       // A lies along K
-    constexpr bool kB = F == Bf16Form::kForward;          // B lies along K
+    constexpr bool kB = F == Bf16Form::kForward || F == Bf16Form::kDown;         // B lies along K
     constexpr bool kRows = F != Bf16Form::kWeightGrad;    // groups own rows of C
+    constexpr bool kGroups = F == Bf16Form::kDataGrad || F == Bf16Form::kDown;   // more than one
     const Bf16Problem& p = s.p;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -71,7 +72,7 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
     const bool rest = kRows && MB == 2 && s.rounds;       // quarters of what the large kernel left
     const int ntl = (int)((p.N + 255) / 256);
     int mtiles = 0, units, left = 0;
-    if constexpr (F == Bf16Form::kDataGrad)
+    if constexpr (kGroups)
         mtiles = rest ? count_row_tiles<256>(p.offs, p.G, lane) : count_row_tiles<SM_M>(p.offs, p.G, lane);
     else
         mtiles = (int)((p.M + (rest ? 256 : SM_M) - 1) / (rest ? 256 : SM_M));
@@ -91,13 +92,13 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
         int mt, nt;
         if (rest) {
             const int t = left + unit / 4;
-            if constexpr (F == Bf16Form::kDataGrad) rg = find_row_group<256>(p.offs, p.G, t / ntl, lane);
+            if constexpr (kGroups) rg = find_row_group<256>(p.offs, p.G, t / ntl, lane);
             const TileAt to = band_order(t - rg.first * ntl, rg.tiles, ntl);
             mt = to.m * 2 + (unit >> 1 & 1);
             nt = to.n * 2 + (unit & 1);
             if (nt >= ntn) return;
         } else {
-            if constexpr (F == Bf16Form::kDataGrad) rg = find_row_group<SM_M>(p.offs, p.G, unit / ntn, lane);
+            if constexpr (kGroups) rg = find_row_group<SM_M>(p.offs, p.G, unit / ntn, lane);
             const TileAt to = band_order(unit - rg.first * ntn, rg.tiles, ntn);
             mt = to.m;
             nt = to.n;
@@ -124,11 +125,11 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
 
     // ---- direct loads ----
     const int64_t lda = kA ? p.K : p.M, ldb = kB ? p.K : p.N;
-    const uint16_t* const Bg = F == Bf16Form::kDataGrad ? p.B + (int64_t)g * p.K * p.N
+    const uint16_t* const Bg = kGroups ? p.B + (int64_t)g * p.K * p.N
                                : F == Bf16Form::kWeightGrad ? p.B + row0 * p.N : p.B;
     const uint16_t* const Ag = F == Bf16Form::kWeightGrad ? p.A + row0 * p.M : p.A;
     // (along K; the adapter linear may take its rows in another order)
-    const int32_t* const order = F == Bf16Form::kForward ? p.lr.order : nullptr;
+    const int32_t* const order = F == Bf16Form::kForward || F == Bf16Form::kDown ? p.lr.order : nullptr;
     const v4i ra = order ? make_rsrc(Ag, p.M * lda * 2) : make_rsrc(Ag + m0 * lda, mvalid * lda * 2);
     const v4i rb = make_rsrc(Bg + n0 * ldb, nvalid * ldb * 2);
     const uint32_t smb = (uint32_t)uni((int)lds_addr(sm));
@@ -332,6 +333,23 @@ __device__ __forceinline__ void small_tile(const SmallArgs& s, const int block,
             }
             return;
         }
+        if constexpr (F == Bf16Form::kDown) {
+            const float sc = p.rscale ? p.rscale[g] : 1.f;
+            v16f lo[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    uint32_t h, l;
+                    split2(av[j][v] * sc, h, l);
+                    av[j][v] = bf16_to_f32(h);
+                    lo[j][v] = bf16_to_f32(l);
+                }
+            uint8_t* const to = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.C) + rw * (2 * p.N) + cw);
+            store_bf16_32x64<false>(av[0], av[1], 1.f, to, (uint32_t)p.N * 4u, rows, cols, lane);
+            store_bf16_32x64<false>(lo[0], lo[1], 1.f, to + p.N * 2, (uint32_t)p.N * 4u, rows, cols, lane);
+            return;
+        }
         uint8_t* const at = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.C) + g * gstride + rw * p.N + cw);
         if (F == Bf16Form::kDataGrad && p.rscale) {
             if (p.drp && cols > 0) {
@@ -377,6 +395,13 @@ bf16_forward_down_kernel(SmallArgs s, LoraDown d, int tiles) {
     const int b = (int)blockIdx.x - tiles, ranks = d.r / 4;
     if (b < 0) return small_tile<Bf16Form::kForward, MB, ST>(s, (int)blockIdx.x, sm.tile);
     lora_down<4, 1, true>(d, b / (4 * ranks), b / 4 % ranks, b % 4, sm.sum);
+}
+
+// The adapters' down projection of sorted rows, adapters as groups.
+__global__ void __launch_bounds__(256, 2)
+bf16_down_kernel(SmallArgs s) {
+    __shared__ __attribute__((aligned(16))) uint8_t sm[3][small_stage(1)];
+    small_tile<Bf16Form::kDown, 1, 3>(s, (int)blockIdx.x, sm);
 }
 
 // ---- sums of the shares ------------------------------------------------------------
@@ -571,7 +596,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t small_tiles(const Bf16Problem& p, int MB) {
     const int64_t ntn = cdiv(p.N, SM_N), bm = small_m(MB);
     if (p.form == Bf16Form::kForward) return cdiv(p.M, bm) * ntn;
-    if (p.form == Bf16Form::kDataGrad)       // sum of ceil(rows / bm) <= this
+    if (p.form == Bf16Form::kDataGrad || p.form == Bf16Form::kDown)     // sum of ceil(rows / bm) <= this
         return (p.rows < p.G ? p.rows : p.G + (p.rows - p.G) / bm) * ntn;
     return (int64_t)p.G * cdiv(p.M, bm) * ntn;
 }
@@ -705,6 +730,23 @@ hipError_t launch_jobs(GradJobs& j, const Plan& d, hipStream_t st) {
 }
 
 }  // namespace
+
+hipError_t launch_lora_down_tiles(const LoraDown& d, hipStream_t st) {
+    Bf16Problem p{};
+    p.form = Bf16Form::kDown;
+    p.G = d.L;
+    p.rows = d.M;
+    p.M = d.M; p.N = d.r; p.K = d.K;
+    p.offs = d.offs;
+    p.A = d.x;
+    p.B = d.a;
+    p.C = d.h;
+    p.rscale = d.scale;
+    p.lr.order = d.order;
+    const unsigned grid = (unsigned)(cdiv(small_tiles(p, 1), 128) * 128);
+    hipLaunchKernelGGL(bf16_down_kernel, dim3(grid), dim3(256), 0, st, SmallArgs{p, 1, false, 0});
+    return hipGetLastError();
+}
 
 hipError_t launch_lora_product(const Bf16Problem& p, const LoraDown& d, hipStream_t st) {
     const Plan q = plan_of(p);

@@ -228,6 +228,8 @@ enum class Bf16Form : int {
     kDataGrad = 1,     // A [M][K] along, B [G][K][N] across, rows by group (dx = dy w)
     kWeightGrad = 2,   // A [rows][M] across, B [rows][N] across, K = a group's rows
                        //   (dw = dy^T x), C [G][M][N]
+    kDown = 3,         // A [M][K] along, rows by group and in lr.order, B [G][N][K] along
+                       //   (h = scale x a^T), C [M][2 N]: high and low bf16 parts
 };
 // Low-rank adapters beside the product: row m with id[m] = l in [0, L) gets
 // h[m] b[l]^T.  h: [M][2 r] bf16, r high and r low parts of each value.
@@ -243,8 +245,9 @@ struct LowRank {
 // launch_lora_sort.
 constexpr int kLoraUnsorted = 256;     // up to so many rows never are
 bool lora_sorts(int64_t M, int64_t K, int L);
+// offs [L + 1]: where the rows of each adapter begin (after the last, those without one).
 hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int L, int32_t* order, int32_t* sorted_ids,
-                            hipStream_t s);
+                            int64_t* offs, hipStream_t s);
 struct Bf16Problem {
     Bf16Form form;
     const int64_t* offs;     // [G + 1] groups of rows (kForward: null, one group of M)
@@ -254,11 +257,11 @@ struct Bf16Problem {
     const uint16_t *A, *B;
     void* C;                 // bf16, or fp32 where c_f32
     bool c_f32, c_add;       // c_add (fp32): added to C
-    const float* rscale;     // kDataGrad: factor of each output row, or null
+    const float* rscale;     // kDataGrad: factor of each output row, kDown: of each group, or null
     const uint16_t* drx;     // kDataGrad with rscale: x [M][N], and
     float* drp;              //   partial sums of x C / rscale, [bf16_dr_parts][M],
     float* dr;               //   their sum [M] (all three null: not computed)
-    LowRank lr;              // kForward
+    LowRank lr;              // kForward (kDown: order)
     float* parts;            // split sums: bf16_parts() floats
 };
 // Rows of the C matrix of each group are M of kWeightGrad, the group's rows else.
@@ -281,11 +284,14 @@ struct LoraDown {
     int64_t M, K;
     const uint16_t* a;
     const int32_t *ids, *order;
+    const int64_t* offs;     // with order: as launch_lora_sort makes it
     const float* scale;
     int L, r;
     uint16_t* h;
 };
 hipError_t launch_lora_down(const LoraDown& p, hipStream_t s);
+// The same in tiles, for rows in order.
+hipError_t launch_lora_down_tiles(const LoraDown& p, hipStream_t s);
 // kForward with its adapters, their h made by d.
 hipError_t launch_lora_product(const Bf16Problem& p, const LoraDown& d, hipStream_t s);
 // The data gradient d and the weight gradient w (either may be null).  scaled (or null):

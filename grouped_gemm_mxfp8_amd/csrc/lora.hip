@@ -22,7 +22,7 @@ constexpr int SORT_THREADS = 1024, kSortMaxL = 8192;
 
 __global__ void __launch_bounds__(SORT_THREADS)
 lora_sort_kernel(const int32_t* __restrict__ ids, int M, int L, int32_t* __restrict__ order,
-                 int32_t* __restrict__ sorted_ids) {
+                 int32_t* __restrict__ sorted_ids, int64_t* __restrict__ offs) {
     __shared__ int s_at[kSortMaxL + 1];           // rows of each adapter, then where the next one goes
     __shared__ int s_wave[SORT_THREADS / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -66,6 +66,7 @@ lora_sort_kernel(const int32_t* __restrict__ ids, int M, int L, int32_t* __restr
     for (int l = beg; l < end; ++l) {
         const int n = s_at[l];
         s_at[l] = at;
+        offs[l] = at;
         at += n;
     }
     __syncthreads();
@@ -410,13 +411,14 @@ bool lora_sorts(int64_t M, int64_t K, int L) {
     return M > kLoraUnsorted && M <= 65536 && L <= kSortMaxL && 8 * (int64_t)L <= M && M * K < ((int64_t)1 << 30);
 }
 hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int L, int32_t* order, int32_t* sorted_ids,
-                            hipStream_t s) {
-    hipLaunchKernelGGL(lora_sort_kernel, dim3(1), dim3(SORT_THREADS), 0, s, ids, (int)M, L, order, sorted_ids);
+                            int64_t* offs, hipStream_t s) {
+    hipLaunchKernelGGL(lora_sort_kernel, dim3(1), dim3(SORT_THREADS), 0, s, ids, (int)M, L, order, sorted_ids, offs);
     return hipGetLastError();
 }
 
 hipError_t launch_lora_down(const LoraDown& p, hipStream_t s) {
     if (p.M == 0) return hipSuccess;
+    if (p.order && p.M * p.r > kDownTiles) return launch_lora_down_tiles(p, s);
     const unsigned blocks = (unsigned)((p.M + 15) / 16), r = (unsigned)p.r;
     auto go = [&](auto kernel, dim3 grid) { hipLaunchKernelGGL(kernel, grid, dim3(64 * DOWN_WAVES), 0, s, p); };
     // one pass over x for up to 32 ranks, where 16 do not have too few workgroups

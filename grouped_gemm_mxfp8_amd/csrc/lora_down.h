@@ -12,7 +12,8 @@
 // sixteen workgroups in calls small enough for that to fill the GPU (FINE).
 //
 // Calls of many rows sort them by adapter first, so that here and in the product's
-// tiles most blocks of rows have one adapter whatever the batch's order.
+// tiles most blocks of rows have one adapter whatever the batch's order.  Many of those take
+// the tiles of a product instead (bf16_down_kernel), which read x once for 128 ranks.
 #pragma once
 #include "bf16_tiles.h"
 
@@ -22,6 +23,13 @@ namespace {
 // Rows times ranks up to which the dots are spread: 4096 workgroups, of which a prompt's
 // blocks use one in sixteen or 32.
 constexpr int64_t kDownFine = 65536;
+
+// Rows times ranks past which sorted rows take tiles of 64 rows x 128 ranks, though the ranks
+// fill few of the 128: a tile of 64 steps in K takes 26 us however full.  The whole call at 16
+// adapters, K x N = 4096 x 1024, us without tiles and with: 1003 rows of rank 64 50.9 and 51.3,
+// 5001 of rank 16 81.9 and 83.1, of 32 92.3 and 84.9, 16384 rows of rank 16 179 and 177, of 64
+// 281 and 197, of 128 421 and 230.
+constexpr int64_t kDownTiles = 131072;
 
 // The two bf16 parts of f.  (An infinity has no rest: inf - inf would make it a NaN.)
 __device__ __forceinline__ void split2(float f, uint32_t& hi, uint32_t& lo) {

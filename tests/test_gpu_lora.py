@@ -189,6 +189,38 @@ def test_wide_layers_keep_what_is_not_finite(dev, M, K, r):
     assert torch.equal(y[0], clean[0]) and y[1].isnan().all()
 
 
+# down projections in tiles: ranks over one column of tiles, adapters with few rows or none
+@pytest.mark.parametrize("M,K,N,r,L,ids", [
+    (2100, 96, 80, 136, 9, "mixed"), (1030, 1056, 48, 512, 3, "each"), (9000, 64, 32, 16, 700, "each"),
+    (3000, 160, 144, 48, 5, "mixed"), (20000, 32, 16, 8, 40, "mixed"), (2060, 4128, 16, 64, 2, 1),
+    (257, 544, 80, 512, 32, "each"), (4100, 64, 528, 40, 512, 511)])
+def test_down_projection_in_tiles(dev, M, K, N, r, L, ids):
+    x, w, a, b, ids, s = make(M, K, N, r, L, ids, M + K + N, dev)
+    nws = gm.lib().lora_linear_ws_bytes(M, N, K, L, r)
+    ws = torch.full((nws,), 255, dtype=torch.uint8, device=dev)
+    y = gm.lora_linear_fwd(x, w, a, b, ids, scale=s, ws=ws)
+    y1 = gm.lora_linear_fwd(x, w, a, b, ids)
+    torch.cuda.synchronize()
+    check(y, x, w, a, b, ids, s)
+    check(y1, x, w, a, b, ids, None)
+    p = torch.randperm(M, generator=torch.Generator().manual_seed(1)).to(dev)
+    assert torch.equal(gm.lora_linear_fwd(x[p], w, a, b, ids[p], scale=s), y[p])
+
+
+def test_down_projection_in_tiles_keeps_what_is_not_finite(dev):
+    x, w, a, b, ids, s = make(1500, 288, 784, 96, 5, "mixed", 3, dev)
+    ids[0], ids[1], ids[2] = 0, 3, -1
+    clean = gm.lora_linear_fwd(x, w, a, b, ids, scale=s)
+    a[3, 1, 7], a[3, 90], b[3, 5, :] = float("-inf"), float("nan"), float("nan")
+    x[2, 9] = float("nan")
+    y = gm.lora_linear_fwd(x, w, a, b, ids, scale=s)
+    torch.cuda.synchronize()
+    hit = (ids == 3).cpu()
+    hit[2] = True
+    assert torch.equal(y[~hit], clean[~hit])
+    assert y[2].isnan().all() and y[1, 5].isnan()
+
+
 # a long K in shares of middle tiles, more than a CU each: rows sorted, and as they are with
 # the down projection beside the tiles
 @pytest.mark.parametrize("L", [3, 90])
