@@ -721,12 +721,13 @@ mx_status grouped_linear_bwd(const void* dy, const void* x, const int64_t* d_off
 
 // ---- the adapter linear -------------------------------------------------------------
 namespace {
-mx::Bf16Problem lora_problem(int64_t M, int64_t N, int64_t K) {
+mx::Bf16Problem lora_problem(int64_t M, int64_t N, int64_t K, int32_t r) {
     mx::Bf16Problem p{};
     p.form = mx::Bf16Form::kForward;
     p.G = 1;
     p.rows = M;
     p.M = M; p.N = N; p.K = K;
+    p.lr.r = r;
     return p;
 }
 struct LoraWs {
@@ -735,12 +736,12 @@ struct LoraWs {
 LoraWs lora_ws(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r) {
     Carver c;
     LoraWs W{};
-    const size_t sorted = mx::lora_sorts(M, K, L) ? (size_t)M * 4 : 0;
+    const size_t sorted = mx::lora_sorts(M, N, K, L, r) ? (size_t)M * 4 : 0;
     W.h = c.take(M > mx::kLoraFewRows || !mx::lora_fuses(M, r) ? (size_t)(M * r) * 4 : 0);
     W.order = c.take(sorted);
     W.ids = c.take(sorted);
     W.offs = c.take(sorted ? (size_t)(L + 1) * 8 : 0);
-    W.parts = c.take(M > mx::kLoraFewRows ? (size_t)mx::bf16_parts(lora_problem(M, N, K)) * 4 : 0);
+    W.parts = c.take(M > mx::kLoraFewRows ? (size_t)mx::bf16_parts(lora_problem(M, N, K, r)) * 4 : 0);
     W.total = needed_or_none(c.off);
     return W;
 }
@@ -753,7 +754,7 @@ mx_status check_lora_sizes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r
     if (K > kBf16MaxDim || N > kBf16MaxDim || M > kI32Max || r > MX_LORA_MAX_RANK)
         return fail(MX_ERR_UNSUPPORTED,
                     "lora_linear_fwd: needs K and N up to 2^21, M below 2^31 and r up to %d", MX_LORA_MAX_RANK);
-    if (mx::bf16_product_tiles(lora_problem(M, N, K)) > mx::kMaxBf16Tiles || (M + 15) / 16 > mx::kMaxBf16Tiles)
+    if (mx::bf16_product_tiles(lora_problem(M, N, K, r)) > mx::kMaxBf16Tiles || (M + 15) / 16 > mx::kMaxBf16Tiles)
         return fail(MX_ERR_UNSUPPORTED, "lora_linear_fwd: too large for one launch");
     return MX_OK;
 }
@@ -789,7 +790,7 @@ mx_status lora_linear_fwd(const void* x, int64_t M, int64_t K, const void* w, in
     const double flops = 2.0 * M * N * (K + r);    // (and 2 M r K of h)
     mx_status ls;
     int64_t* offs = nullptr;
-    if (mx::lora_sorts(M, K, L)) {
+    if (mx::lora_sorts(M, N, K, L, r)) {
         int32_t *const to = reinterpret_cast<int32_t*>(base + W.order), *const sid = reinterpret_cast<int32_t*>(base + W.ids);
         offs = reinterpret_cast<int64_t*>(base + W.offs);
         ls = launched(timed("lora_sort", 16.0 * M, MX_WORK_BYTES, s,
@@ -814,7 +815,7 @@ mx_status lora_linear_fwd(const void* x, int64_t M, int64_t K, const void* w, in
                               }),
                         "lora_few");
     }
-    mx::Bf16Problem p = lora_problem(M, N, K);
+    mx::Bf16Problem p = lora_problem(M, N, K, r);
     p.A = x16;
     p.B = w16;
     p.C = y;

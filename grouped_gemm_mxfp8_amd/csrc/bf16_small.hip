@@ -626,7 +626,7 @@ Plan plan_rows(const Bf16Problem& p) {
     const int64_t rows = groups ? cdiv(p.rows, groups) : 0;
     const double nk = (double)cdiv(p.K, SM_K);
     auto tiles = [&](int bm, int bn) { return (double)(groups * cdiv(rows, bm) * cdiv(p.N, bn)); };
-    const bool beside = p.form == Bf16Form::kForward && p.rows <= kLoraUnsorted;
+    const bool beside = p.form == Bf16Form::kForward && p.rows <= kLoraUnsorted && few_low_rank(p.rows, p.N, p.lr.r);
     auto tile_us = [&](Kind k, double units, double steps, double cus) {
         const double each = units / cus, most = units <= 2 * cus ? 2 : (double)(((int64_t)units - 1) / (int64_t)cus + 1);
         if (k == kSmall) return steps * (each <= 1 ? 0.31 : 0.30 * most);
@@ -751,9 +751,13 @@ hipError_t launch_lora_down_tiles(const LoraDown& d, hipStream_t st) {
 hipError_t launch_lora_product(const Bf16Problem& p, const LoraDown& d, hipStream_t st) {
     const Plan q = plan_of(p);
     const dim3 bd(256);
-    // The adapters' part in the tiles shares each adapter's b among up to 32 rows, in the
-    // join of a split K every row reads its own.
-    const bool join_lr = q.split > 1 && p.M * p.N * p.lr.r <= (int64_t)1 << 25;
+    // The join adds the adapters' part where that is small, and twice that much for unsorted
+    // rows of many adapters in more than two shares (72 rows, 4096 x 4096, rank 128, us: 16
+    // adapters 74 in the tiles, 50 in the join, 64 adapters 115 and 58; 4 adapters 39 and 45; two
+    // shares of 64 rows, 4096 x 14336, rank 64, 16 adapters 56 and 87).
+    const bool join_lr = q.split > 1 && (few_low_rank(p.M, p.N, p.lr.r) ||
+                                         (q.split > 2 && !d.order && d.L > 4 &&
+                                          p.M * p.N * p.lr.r <= 2 * kFewLowRank));
     // then h can be made beside the tiles
     const bool with_down = join_lr && !d.order && p.M * d.r <= kDownFine;
     hipError_t e = with_down ? hipSuccess : launch_lora_down(d, st);

@@ -243,8 +243,12 @@ struct LowRank {
 };
 // Whether a call's rows are put in the order of their adapters: order and id come from
 // launch_lora_sort.
-constexpr int kLoraUnsorted = 256;     // up to so many rows never are
-bool lora_sorts(int64_t M, int64_t K, int L);
+constexpr int kLoraUnsorted = 256;     // up to so many rows are sorted only where few_low_rank fails
+bool lora_sorts(int64_t M, int64_t N, int64_t K, int L, int r);
+// Whether the adapters' part is small enough for every row to read its own b (where a split K
+// is joined); tiles share each adapter's b among up to 32 rows.
+constexpr int64_t kFewLowRank = (int64_t)1 << 25;
+constexpr bool few_low_rank(int64_t M, int64_t N, int r) { return M * N * r <= kFewLowRank; }
 // offs [L + 1]: where the rows of each adapter begin (after the last, those without one).
 hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int L, int32_t* order, int32_t* sorted_ids,
                             int64_t* offs, hipStream_t s);

@@ -406,9 +406,15 @@ hipError_t launch_lora_few(const uint16_t* x, int64_t M, int64_t K, const uint16
     return hipGetLastError();
 }
 
-// Where adapters have eight rows each on average; rows in 32-bit bytes.
-bool lora_sorts(int64_t M, int64_t K, int L) {
-    return M > kLoraUnsorted && M <= 65536 && L <= kSortMaxL && 8 * (int64_t)L <= M && M * K < ((int64_t)1 << 30);
+// Where adapters have eight rows each on average, of 256 rows on two: the tiles add each
+// adapter among 32 rows for itself.  4096 x 4096, 16 adapters of rank 64, us: 256 single rows
+// 103 unsorted and 43 sorted, three times as many of one adapter after the other 46 and 40;
+// 64 adapters, 400 rows 108 and 70.  Where each row's part is small (few_low_rank), only past
+// 256 rows (rank 16, 400 rows of 64 adapters: 42 unsorted, 55).  Rows in 32-bit bytes.
+bool lora_sorts(int64_t M, int64_t N, int64_t K, int L, int r) {
+    const bool few = few_low_rank(M, N, r);
+    return M > (few ? kLoraUnsorted : 64) && (few || M < 256 ? 8 : 2) * (int64_t)L <= M && M <= 65536 &&
+           L <= kSortMaxL && M * K < ((int64_t)1 << 30);
 }
 hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int L, int32_t* order, int32_t* sorted_ids,
                             int64_t* offs, hipStream_t s) {

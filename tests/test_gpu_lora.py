@@ -221,6 +221,21 @@ def test_down_projection_in_tiles_keeps_what_is_not_finite(dev):
     assert y[2].isnan().all() and y[1, 5].isnan()
 
 
+# high ranks of few rows: sorted from 65 rows on, added in the join or in the tiles
+@pytest.mark.parametrize("M,K,N,r,L,ids", [
+    (72, 1056, 4096, 128, 16, "each"), (72, 1056, 4096, 128, 4, "each"), (64, 544, 2064, 256, 20, "mixed"),
+    (65, 96, 1040, 512, 8, "each"), (200, 288, 4112, 64, 25, "each"), (255, 288, 4112, 40, 32, "each"),
+    (256, 160, 4112, 40, 128, "each"), (257, 160, 4112, 40, 129, "each"), (20, 2080, 14336, 128, 30, "each")])
+def test_high_ranks(dev, M, K, N, r, L, ids):
+    x, w, a, b, ids, s = make(M, K, N, r, L, ids, M + K + N, dev)
+    nws = gm.lib().lora_linear_ws_bytes(M, N, K, L, r)
+    ws = torch.full((nws,), 255, dtype=torch.uint8, device=dev)
+    y = gm.lora_linear_fwd(x, w, a, b, ids, scale=s, ws=ws)
+    torch.cuda.synchronize()
+    check(y, x, w, a, b, ids, s)
+    assert torch.equal(y, gm.lora_linear_fwd(x, w, a, b, ids, scale=s))
+
+
 # a long K in shares of middle tiles, more than a CU each: rows sorted, and as they are with
 # the down projection beside the tiles
 @pytest.mark.parametrize("L", [3, 90])
