@@ -408,7 +408,7 @@ hipError_t launch_lora_few(const uint16_t* x, int64_t M, int64_t K, const uint16
 
 // Where adapters have eight rows each on average, of 256 rows on two: the tiles add each
 // adapter among 32 rows for itself.  4096 x 4096, 16 adapters of rank 64, us: 256 single rows
-// 103 unsorted and 43 sorted, three times as many of one adapter after the other 46 and 40;
+// 103 unsorted and 43 sorted, the same in runs of one adapter 46 and 40;
 // 64 adapters, 400 rows 108 and 70.  Where each row's part is small (few_low_rank), only past
 // 256 rows (rank 16, 400 rows of 64 adapters: 42 unsorted, 55).  Rows in 32-bit bytes.
 bool lora_sorts(int64_t M, int64_t N, int64_t K, int L, int r) {
