@@ -701,6 +701,18 @@ int64_t bf16_product_tiles(const Bf16Problem& p) {
 
 int64_t bf16_dr_parts(int64_t N) { return cdiv(N, 64); }
 
+extern "C" int32_t mx_internal_bf16_plan(int32_t form, int32_t G, int64_t rows, int64_t M, int64_t N, int64_t K,
+                                         int32_t r) {
+    Bf16Problem p{};
+    p.form = (Bf16Form)form;
+    p.G = G;
+    p.rows = rows;
+    p.M = M; p.N = N; p.K = K;
+    p.lr.r = r;
+    const Plan q = plan_of(p);
+    return q.kind + 4 * q.split;
+}
+
 namespace {
 
 // Workgroups of the middle tiles that take what the large kernel left, where only the

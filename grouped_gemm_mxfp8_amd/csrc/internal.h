@@ -276,6 +276,10 @@ constexpr int64_t kMaxBf16Tiles = (int64_t)1 << 22;
 int64_t bf16_product_tiles(const Bf16Problem& p);
 int64_t bf16_parts(const Bf16Problem& p);
 int64_t bf16_dr_parts(int64_t N);
+// Which kernel a product takes, for tests (rows, G and lr.r where its form has them): 0 large,
+// 1 small, 2 middle tiles, plus 4 times the shares of K.
+extern "C" int32_t mx_internal_bf16_plan(int32_t form, int32_t G, int64_t rows, int64_t M, int64_t N, int64_t K,
+                                         int32_t r);
 // The kernels it chooses from: 256 x 256 tiles (tail: only whole rounds of them, see
 // whole_rounds; the rest is then the middle tiles'), bf16_large_grid() workgroups.
 int bf16_large_grid();
