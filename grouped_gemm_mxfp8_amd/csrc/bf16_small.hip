@@ -636,7 +636,12 @@ Plan plan_rows(const Bf16Problem& p) {
     double least = 1e30;
     for (Kind k : {kSmall, kMiddle}) {
         const double t = tiles(small_m(k), SM_N);
-        for (int split = 1; split <= 16 && nk >= 4.0 * split && t * split <= 1024; ++split) {
+        // Sums of one to three steps are starting and storing, half as long for a small tile:
+        // middle ones only where small ones take a second round (us, small and middle: x w^T
+        // of 456 rows, K x N = 64 x 4176 10.4 and 12.2, 4096 rows, 128 x 4096 24.9 and 22.3)
+        if (k == kMiddle && nk < 4 && tiles(small_m(kSmall), SM_N) <= 512) continue;
+        // (a share keeps four steps)
+        for (int split = 1; split == 1 || (split <= 16 && nk >= 4.0 * split && t * split <= 1024); ++split) {
             double us = 6 + tile_us(k, t * split, nk / split, beside && split > 1 ? 128 : 256);
             if (beside && split == 1) us += p.K / 512;
             if (split > 1) us += 4.5 + 8e-6 * split * p.rows * p.N / 3;
@@ -644,11 +649,6 @@ Plan plan_rows(const Bf16Problem& p) {
                 least = us;
                 best = Plan{k, split, small_tiles(p, k) * split <= 256};
             }
-        }
-        const double whole = 6 + tile_us(k, t, nk, 256);
-        if (t > 1024 && whole < least) {
-            least = whole;
-            best = Plan{k, 1, false};
         }
     }
     const double t = tiles(256, 256);

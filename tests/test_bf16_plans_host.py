@@ -46,3 +46,16 @@ def test_data_gradient_reaches_the_large_tiles(plan, counts, N, K):
 @pytest.mark.parametrize("M,K,N,r,L,ids", T.UNSORTED)
 def test_down_projection_stays_unsorted_and_unspread(plan, mxlib, M, K, N, r, L, ids):
     assert plan(FORWARD, 1, M, M, N, K, r)[1] == 1 and unsorted(mxlib, M, K, N, r, L) and M * r > 65536
+
+
+@pytest.mark.parametrize("form,G,M,N,K,kind", [
+    # 1024 middle tiles of two steps, and 2048 small ones
+    (FORWARD, 1, 4096, 4096, 128, MIDDLE), (DATA_GRAD, 1, 4096, 4096, 16, MIDDLE),
+    # as many of three; fewer than a GPU has room for: small ones
+    (FORWARD, 1, 8192, 2048, 192, MIDDLE), (FORWARD, 1, 300, 2048, 64, SMALL), (DATA_GRAD, 4, 512, 128, 64, SMALL),
+    # more than 1024 middle tiles, more than 1024 small tiles of few rows each
+    (DATA_GRAD, 4, 52000, 32, 16, MIDDLE), (DATA_GRAD, 28, 96, 2080, 128, SMALL), (DATA_GRAD, 9, 5, 12992, 64, SMALL),
+])
+def test_short_sums_take_the_faster_tiles_too(plan, form, G, M, N, K, kind):
+    """Sums of up to three steps: no shares of K, and both kinds of tiles are considered."""
+    assert plan(form, G, M, M, N, K, 8) == (kind, 1)
