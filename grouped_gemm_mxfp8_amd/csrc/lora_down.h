@@ -31,9 +31,12 @@ constexpr int64_t kDownFine = 65536;
 // 281 and 197, of 128 421 and 230.
 constexpr int64_t kDownTiles = 131072;
 
-// The two bf16 parts of f.  (An infinity has no rest: inf - inf would make it a NaN.)
+// The two bf16 parts of f.  A finite value past bf16's largest, which rounding would make an
+// infinity, is cut off instead: its rest is below 2^-7 of it, and with it the two are off by at
+// most 2^-16 as elsewhere.  (An infinity has no rest: inf - inf would make it a NaN.)
 __device__ __forceinline__ void split2(float f, uint32_t& hi, uint32_t& lo) {
     hi = f32_to_bf16(f);
+    if ((hi & 0x7fffu) == 0x7f80u && __builtin_isfinite(f)) hi = __float_as_uint(f) >> 16;
     const float rest = f - bf16_to_f32(hi);
     lo = __builtin_isfinite(rest) ? f32_to_bf16(rest) : 0u;
 }
