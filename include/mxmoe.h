@@ -235,7 +235,10 @@ mx_status grouped_linear_bwd(const void* dy, const void* x, const int64_t* d_off
  *          a call that may run at the same time; may be NULL where that is 256, which
  *          means none.
  * Adapters are trained as two GroupedLinears with rows sorted by adapter (a and b as w)
- * and their grouped_linear_bwd.
+ * and their grouped_linear_bwd.  Those need r % 32 == 0 (b's K and a's N): other ranks
+ * are padded with zeros to the next multiple of 32, a's rows and b's columns.  The
+ * padding's gradients are exact zeros, so it stays zero, and the padded weights are
+ * served here as they are.
  */
 #define MX_LORA_MAX_RANK 512
 size_t lora_linear_ws_bytes(int64_t M, int64_t N, int64_t K, int32_t L, int32_t r);
