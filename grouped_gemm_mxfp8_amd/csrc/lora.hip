@@ -17,7 +17,8 @@ lora_down_kernel(LoraDown p) {
 
 // ---- rows by adapter -----------------------------------------------------------------
 // A counting sort in one workgroup.  The order among an adapter's rows is that of LDS
-// atomics, any: no row's result depends on the rows beside it.
+// atomics, any: sorted rows always take the MFMA, where no row's result depends on the rows
+// beside it.
 constexpr int SORT_THREADS = 1024, kSortMaxL = 8192;
 
 __global__ void __launch_bounds__(SORT_THREADS)

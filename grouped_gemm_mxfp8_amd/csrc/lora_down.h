@@ -88,8 +88,10 @@ __device__ __forceinline__ void lora_down(const LoraDown& p, const int bx, const
     };
 
     // Spread dots also serve a block with few rows: one adapter on the MFMA takes a workgroup
-    // 7 us (K = 4096) however few there are.  (Sorted rows always go to the MFMA: a row's sums are then the same whatever rows are
-    // beside it, and with them the same for any order among an adapter's rows.)
+    // 7 us (K = 4096) however few there are.  The two add in different orders, so the last bits of
+    // a row's h go by the adapters beside it.  (Sorted rows always go to the MFMA: a row's sums are
+    // then the same whatever rows are beside it, and with them the same for any order among an
+    // adapter's rows.)
     if (!p.order && (kinds > 2 || (FINE && __popcll(left) <= 32))) {
         // FINE: by counts ranks in fours, bz rows in fours; else ranks in 16 RB, all rows
         constexpr int RANKS = FINE ? 4 : 16 * RB, PARTS = WAVES / 4;

@@ -225,9 +225,10 @@ mx_status grouped_linear_bwd(const void* dy, const void* x, const int64_t* d_off
  *
  *   x bf16 [M][K], w bf16 [N][K], a bf16 [L][r][K], b bf16 [L][N][r], d_ids int32 [M],
  *   d_scale fp32 [L] or NULL (1), y bf16 [M][N].
- *   Sums in fp32 in one fixed order; s A x goes on as two bf16 values (high and low
- *   part, off by at most 2^-16 of it); y is rounded once.  Adapters of smaller rank: zeros in
- *   a's further rows (or b's further columns).
+ *   Sums in fp32, in an order that the sizes and ids fix: two calls give the same bits.
+ *   (The same row in another batch may be summed in another order.)  s A x goes on as two
+ *   bf16 values (high and low part, off by at most 2^-16 of it); y is rounded once.
+ *   Adapters of smaller rank: zeros in a's further rows (or b's further columns).
  *   K % 32 == 0, N % 16 == 0, r % 8 == 0, K and N up to 2^21, r up to
  *   MX_LORA_MAX_RANK (MX_ERR_UNSUPPORTED otherwise); x, w, a, b and y 16-byte aligned;
  *   y and ws must not overlap inputs.  Nothing is allocated.

@@ -75,3 +75,22 @@ def test_adapters_of_other_ranks_trained_with_zeros(dev, r):
     assert (np.abs(d - ref) <= 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * (N + 2) * 2.0 ** -23 * mag).all()
     args = (to64(x), w64, a64, b64, ids.cpu().numpy())
     assert (np.abs(to64(y) - B.lora_fwd(*args)) <= B.lora_bound(*args)).all()
+
+
+@pytest.mark.parametrize("M,L", [(40, 5), (200, 90), (12, 12)])
+def test_unsorted_rows_are_right_in_any_order(dev, M, L):
+    """Rows as they are, in four orders: dots or MFMA blocks go by the adapters among sixteen
+    rows, so a row's last bits may differ, within the bounds, and the same call repeats itself."""
+    g = torch.Generator().manual_seed(M)
+    K, N, r = 544, 272, 16
+    rnd = lambda *s: torch.randn(s, generator=g)
+    x, w = rnd(M, K).bfloat16(), (0.05 * rnd(N, K)).bfloat16()
+    a, b = (rnd(L, r, K) * K ** -0.5).bfloat16(), (0.3 * rnd(L, N, r)).bfloat16()
+    ids = torch.randint(-1, L, (M,), generator=g).int()
+    args = [to64(t) for t in (x, w, a, b)] + [ids.numpy()]
+    ref, bound = B.lora_fwd(*args), B.lora_bound(*args)
+    for p in (torch.arange(M), ids.argsort(), torch.randperm(M, generator=g), torch.randperm(M, generator=g)):
+        call = [t.to(dev) for t in (x[p], w, a, b, ids[p])]
+        y = gm.lora_linear_fwd(*call)
+        assert torch.equal(y, gm.lora_linear_fwd(*call))
+        assert (np.abs(to64(y) - ref[p]) <= bound[p]).all()
