@@ -664,10 +664,11 @@ Plan plan_rows(const Bf16Problem& p) {
 
 // Weight gradients: the large tiles' chains hide the stores that take most of the time
 // where groups have few rows, but a few rounds of them wait for the group with most rows
-// (8 experts of 2816 x 1024, 16384 rows falling as 1 / rank^1.1: 174 us, middle tiles
-// 113; even: 112 and 111).  One group has no such thing, only a last round partly used
+// (8 experts of 2816 x 1024, 16384 rows falling as 1 / rank^1.1: 165 us, middle tiles
+// 122; even: 109 and 111).  One group has no such thing, only a last round partly used
 // (4096 x 4096, 2048 rows: 59 us, middle 75).  Middle tiles split long sums where there
-// are few (8 of 512 x 512, 16384 rows: 27 us, large 52).
+// are few (8 of 512 x 512, 16384 rows: 27 us, large 52).  How many shares goes by groups of
+// equal rows: one group with all of them keeps a long sum (81 us there, even 22).
 Plan plan_weights(const Bf16Problem& p) {
     const int64_t large = p.G * cdiv(p.M, 256) * cdiv(p.N, 256);
     const int64_t last = large % 256;

@@ -409,9 +409,11 @@ hipError_t launch_lora_few(const uint16_t* x, int64_t M, int64_t K, const uint16
 
 // Where adapters have eight rows each on average, of 256 rows on two: the tiles add each
 // adapter among 32 rows for itself.  4096 x 4096, 16 adapters of rank 64, us: 256 single rows
-// 103 unsorted and 43 sorted, the same in runs of one adapter 46 and 40;
-// 64 adapters, 400 rows 108 and 70.  Where each row's part is small (few_low_rank), only past
-// 256 rows (rank 16, 400 rows of 64 adapters: 42 unsorted, 55).  Rows in 32-bit bytes.
+// 66 unsorted and 52 sorted, of rank 128 112 and 59; 64 adapters of rank 64, 400 rows 119 and
+// 80; rank 16, 4096 rows 199 and 140.  Where each row's part is small (few_low_rank), only past
+// 256 rows (rank 16, 400 rows of 64 adapters: 42 unsorted, 55).  Rows in 32-bit bytes; and up to
+// 65536 of them, as one workgroup sorts (65600 single rows of 16 adapters, 4096 x 1024, unsorted:
+// rank 16 1199, 65536 sorted 652; rank 128 7799 and 816).
 bool lora_sorts(int64_t M, int64_t N, int64_t K, int L, int r) {
     const bool few = few_low_rank(M, N, r);
     return M > (few ? kLoraUnsorted : 64) && (few || M < 256 ? 8 : 2) * (int64_t)L <= M && M <= 65536 &&
